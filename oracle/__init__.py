@@ -13,6 +13,8 @@ It is a plain, slow, obviously-correct restatement of what the method computes:
   and backward, in float64.
 * ``oracle.optim`` — the AdamW step of the LoRA factors and the rank-stabilized
   scale.
+* ``oracle.norm_w4`` — the RMS norm, its 8-bit rows and gradient, and the packed
+  4-bit group-scaled weight.
 * ``oracle.dq``   — double quantization of the NF4 block scales (8-bit E4M3
   codes in blocks of 256).
 
@@ -21,4 +23,4 @@ forms, independent library routines, exact rational brute force and finite
 differences. Parity unpinned: equality with any third-party NF4 table or file
 format (the pages give no worked example of one).
 """
-from . import dq, lora, nf4, optim  # noqa: F401
+from . import dq, lora, nf4, norm_w4, optim  # noqa: F401

@@ -18,6 +18,9 @@ library has not been built, the first call raises.
     q, sc, off = nf4_absmax_quantize(absmax)                     # 8-bit block scales
     absmax2 = nf4_absmax_dequantize(q, sc, off).view_as(absmax)
     alpha_rs = rslora_alpha(lora_alpha, r)                       # scale alpha / sqrt(r)
+
+The RMS norm before the linear and the 4-bit group-scaled product that serves a merged
+weight (C ABI in include/norm_w4.h) are in the submodule norm_w4 and exported here too.
 """
 from __future__ import annotations
 
@@ -533,3 +536,9 @@ def nf4_absmax_dequantize(q, scale, offset):
     _check("nf4_absmax_dequantize", library().nf4_absmax_dequantize(
         q.data_ptr(), scale.data_ptr(), offset.data_ptr(), n, out.data_ptr(), _stream(q)))
     return out
+
+
+from .norm_w4 import *  # noqa: E402,F401,F403  (registers its entry points with library())
+from . import norm_w4 as _norm_w4  # noqa: E402
+
+__all__ += _norm_w4.__all__

@@ -7,6 +7,7 @@
 #include <cstdint>
 #include <mutex>
 
+#include "api_check.h"
 #include "launch.h"
 #include "lora_nf4.h"
 
@@ -19,31 +20,7 @@ bool weight_staging() { return g_weight_staging.load(std::memory_order_relaxed);
 
 namespace {
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-struct Span {
-  const void* p;
-  size_t bytes;
-};
-
-bool overlap(const Span& a, const Span& b) {
-  if (a.p == nullptr || b.p == nullptr || a.bytes == 0 || b.bytes == 0) return false;
-  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a.p), b0 = reinterpret_cast<uintptr_t>(b.p);
-  return a0 < b0 + b.bytes && b0 < a0 + a.bytes;
-}
-
-// Every output span must be disjoint from every input span and from the other outputs.
-bool any_alias(const Span* outs, int n_out, const Span* ins, int n_in) {
-  for (int i = 0; i < n_out; ++i) {
-    for (int j = 0; j < n_in; ++j)
-      if (overlap(outs[i], ins[j])) return true;
-    for (int j = i + 1; j < n_out; ++j)
-      if (overlap(outs[i], outs[j])) return true;
-  }
-  return false;
-}
-
-constexpr int64_t kMaxDim = (int64_t(1) << 31) - 1;
+using namespace lnf4;
 
 // Shared shape rules of the forward and backward (T = 0 is an empty batch).
 int check_linear_shape(int64_t T, int64_t K, int64_t N, int32_t r, float alpha) {
@@ -54,8 +31,6 @@ int check_linear_shape(int64_t T, int64_t K, int64_t N, int32_t r, float alpha) 
   if (T > kMaxDim || K > kMaxDim || N > kMaxDim) return LN_ESHAPE;
   return LN_OK;
 }
-
-int hip_status(hipError_t e) { return e == hipSuccess ? LN_OK : LN_EHIP; }
 
 }  // namespace
 

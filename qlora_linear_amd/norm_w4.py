@@ -1,0 +1,246 @@
+"""The operators around the NF4-LoRA linear (C ABI in include/norm_w4.h): the RMS norm
+with the residual's addition, its gradient and its 8-bit output, and the product with
+a 4-bit group-scaled weight.
+
+    y, h, rstd = rmsnorm_fwd(x, w, residual=res)                  # h = x + res, y = norm(h) w
+    dx, dw = rmsnorm_bwd(dy, h, w, rstd, dh=dh)                   # dx: of x and of res
+    q, scale, h = rmsnorm_fwd_quant(x, w, residual=res)           # 8-bit rows, one scale each
+    packed = w4_quantize(lora_nf4_merge(codes, absmax, A, B, lora_alpha), group=128)
+    y = w4_matvec(q, *packed, d_out=d_out, x_scale=scale)         # (codes, scales, zeros)
+
+Like the rest of the binding these functions only check and marshal their arguments,
+allocate the outputs and call the C entry point of the same name on the current stream
+of the tensors' device. They make one launch or two each and may be captured into a
+graph. Gradients are functions of their own, not autograd nodes.
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from . import LN_BF16, LN_F32, LN_MAX_PROJ, LN_OK, LoraNF4Error, _SIGS, _workspace, library
+
+__all__ = ["rmsnorm_fwd", "rmsnorm_fwd_quant", "rmsnorm_bwd", "rmsnorm_bwd_workspace_bytes", "w4_quantize",
+           "w4_dequantize", "w4_matvec", "w4_matvec_multi", "NORM_W4_SYMBOLS", "LN_E4M3", "LN_I8"]
+
+LN_E4M3, LN_I8 = 2, 3
+
+_p, _i, _i64, _i32, _f = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_int32, ctypes.c_float
+_NORM_W4_SIGS = {
+    "rmsnorm_fwd": (_i, [_i64, _i64, _i, _f, _p, _p, _p, _p, _p, _p, _p]),
+    "rmsnorm_fwd_quant": (_i, [_i64, _i64, _i, _f, _p, _p, _p, _p, _i, _p, _p, _p]),
+    "rmsnorm_bwd": (_i, [_i64, _i64, _i, _p, _p, _p, _p, _p, _p, _p, _p, ctypes.c_size_t, _p]),
+    "rmsnorm_bwd_workspace_bytes": (ctypes.c_size_t, [_i64, _i64]),
+    "w4_quantize": (_i, [_p, _i, _i64, _i64, _i32, _p, _p, _p, _p]),
+    "w4_dequantize": (_i, [_p, _p, _p, _i64, _i64, _i32, _i, _p, _p]),
+    "w4_matvec": (_i, [_i64, _i64, _i64, _i32, _i, _p, _p, _p, _p, _p, _i, _p, _p]),
+    "w4_matvec_multi": (_i, [_i64, _i64, _i32, _p, _i32, _i, _p, _p, _p, _p, _p, _i, _p, _p]),
+}
+_SIGS.update(_NORM_W4_SIGS)
+NORM_W4_SYMBOLS = tuple(_NORM_W4_SIGS)
+
+_PLAIN = {torch.float32: LN_F32, torch.bfloat16: LN_BF16}
+_EIGHT = {torch.float8_e4m3fn: LN_E4M3, torch.int8: LN_I8}
+_X = {torch.bfloat16: LN_BF16, **_EIGHT}
+
+
+def _code(table, dtype, name):
+    try:
+        return table[dtype]
+    except KeyError:
+        raise ValueError(f"{name} must have one of the dtypes {[str(t) for t in table]}, got {dtype}") from None
+
+
+def _lead(t, name, ndim):
+    """The device index of the tensor that decides where a call runs."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor")
+    if t.dim() != ndim:
+        raise ValueError(f"{name} must be {ndim}-D")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.get_device()
+
+
+def _like(t, name, dev, dtype, shape):
+    """The address of an operand on device `dev`, of a dtype and shape; None stays None."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.get_device() != dev:
+        raise ValueError(f"{name} must be a tensor on GPU {dev}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must have dtype {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _call(name, dev, *args):
+    """The C entry point on the current stream of device `dev` (made the current device
+    for the launch, where it is not)."""
+    fn = getattr(library(), name)
+    if torch.cuda.current_device() == dev:
+        st = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    if st != LN_OK:
+        raise LoraNF4Error(name, st)
+
+
+def _norm_args(x, weight, residual):
+    dev = _lead(x, "x", 2)
+    kind = _code(_PLAIN, x.dtype, "x")
+    T, d = x.shape
+    w = _like(weight, "weight", dev, x.dtype, (d,))
+    if w is None:
+        raise ValueError("weight must be given")
+    r = _like(residual, "residual", dev, x.dtype, x.shape)
+    return dev, kind, T, d, w, r
+
+
+def rmsnorm_fwd(x, weight, eps: float = 1e-5, residual=None, save_rstd: bool = True):
+    """(y, h, rstd): h = x + residual rounded to x's dtype (x itself without a residual),
+    y = h * rstd * weight, rstd = 1 / sqrt(mean(h^2) + eps) float32 [T] (None unless
+    save_rstd). x [T, d] float32 or bf16; weight [d] and residual [T, d] of the same dtype."""
+    dev, kind, T, d, w, r = _norm_args(x, weight, residual)
+    y = torch.empty_like(x)
+    h = x if residual is None else torch.empty_like(x)
+    rstd = torch.empty(T, dtype=torch.float32, device=x.device) if save_rstd else None
+    _call("rmsnorm_fwd", dev, T, d, kind, eps, x.data_ptr(), r, w, None if r is None else h.data_ptr(),
+          y.data_ptr(), None if rstd is None else rstd.data_ptr())
+    return y, h, rstd
+
+
+def rmsnorm_fwd_quant(x, weight, eps: float = 1e-5, residual=None, qdtype=torch.float8_e4m3fn):
+    """(q, scale, h): the norm's rows as qdtype (torch.float8_e4m3fn or torch.int8) [T, d] and
+    one float32 scale a row [T], y = q * scale; h as for rmsnorm_fwd."""
+    dev, kind, T, d, w, r = _norm_args(x, weight, residual)
+    fmt = _code(_EIGHT, qdtype, "qdtype")
+    q = torch.empty_like(x, dtype=qdtype)
+    scale = torch.empty(T, dtype=torch.float32, device=x.device)
+    h = x if residual is None else torch.empty_like(x)
+    _call("rmsnorm_fwd_quant", dev, T, d, kind, eps, x.data_ptr(), r, w, None if r is None else h.data_ptr(), fmt,
+          q.data_ptr(), scale.data_ptr())
+    return q, scale, h
+
+
+def rmsnorm_bwd_workspace_bytes(T: int, d: int) -> int:
+    return int(library().rmsnorm_bwd_workspace_bytes(T, d))
+
+
+def rmsnorm_bwd(dy, h, weight, rstd, dh=None, need_dw: bool = True, workspace: torch.Tensor | None = None):
+    """(dx, dw or None) of rmsnorm_fwd for the gradient dy of y and, if given, the gradient dh
+    that reaches h from its other readers; dx is the gradient of x and of the residual."""
+    dev = _lead(h, "h", 2)
+    kind = _code(_PLAIN, h.dtype, "h")
+    T, d = h.shape
+    w = _like(weight, "weight", dev, h.dtype, (d,))
+    g = _like(dy, "dy", dev, h.dtype, h.shape)
+    r = _like(rstd, "rstd", dev, torch.float32, (T,))
+    if w is None or g is None or r is None:
+        raise ValueError("dy, weight and rstd must be given")
+    e = _like(dh, "dh", dev, h.dtype, h.shape)
+    dx = torch.empty_like(h)
+    dw = torch.empty_like(weight) if need_dw else None
+    ws = _workspace(rmsnorm_bwd_workspace_bytes(T, d), workspace, h.device) if need_dw else None
+    _call("rmsnorm_bwd", dev, T, d, kind, g, e, h.data_ptr(), w, r, dx.data_ptr(),
+          None if dw is None else dw.data_ptr(), None if ws is None else ws.data_ptr(),
+          0 if ws is None else ws.numel())
+    return dx, dw
+
+
+def w4_quantize(w, group: int = 128, zero_points: bool = False):
+    """(codes, scales, zeros or None): w [d_out, d_in] float32 or bf16 packed to 4 bits with one
+    bf16 scale (and zero point) per row and `group` columns (32, 64 or 128; d_in a multiple of
+    64 and of group), laid out in tiles of 16 rows x 128 columns as norm_w4.h describes."""
+    dev = _lead(w, "w", 2)
+    kind = _code(_PLAIN, w.dtype, "w")
+    N, K = w.shape
+    if group not in (32, 64, 128):
+        raise ValueError(f"group must be 32, 64 or 128, got {group}")
+    nt, kt, kg = (N + 15) // 16, (K + 127) // 128, K // group
+    codes = torch.empty((nt, kt, 1024), dtype=torch.uint8, device=w.device)
+    scales = torch.empty((nt, kg, 16), dtype=torch.bfloat16, device=w.device)
+    zeros = torch.empty((nt, kg, 16), dtype=torch.uint8, device=w.device) if zero_points else None
+    _call("w4_quantize", dev, w.data_ptr(), kind, N, K, group, codes.data_ptr(), scales.data_ptr(),
+          None if zeros is None else zeros.data_ptr())
+    return codes, scales, zeros
+
+
+def _packed(codes, scales, zeros, d_in, d_out, dev, tag=""):
+    """(d_out, group, addresses) of a packed weight whose rows are d_in wide."""
+    if not isinstance(scales, torch.Tensor) or scales.dim() != 3 or not scales.shape[1]:
+        raise ValueError(f"scales{tag} must be [ceil(d_out / 16), d_in / group, 16]")
+    nt, kg = scales.shape[:2]
+    group = d_in // kg
+    if kg * group != d_in or group not in (32, 64, 128):
+        raise ValueError(f"scales{tag} hold {kg} groups of a row: d_in {d_in} makes no group of 32, 64 or 128")
+    if d_out is None:
+        d_out = 16 * nt
+    if not 16 * (nt - 1) < d_out <= 16 * nt:
+        raise ValueError(f"d_out{tag} {d_out} does not fit scales{tag} of {nt} tiles of 16 rows")
+    c = _like(codes, f"codes{tag}", dev, torch.uint8, (nt, (d_in + 127) // 128, 1024))
+    s = _like(scales, f"scales{tag}", dev, torch.bfloat16, (nt, kg, 16))
+    z = _like(zeros, f"zeros{tag}", dev, torch.uint8, (nt, kg, 16))
+    if c is None:
+        raise ValueError(f"codes{tag} must be given")
+    return d_out, group, c, s, z
+
+
+def w4_dequantize(codes, scales, zeros=None, *, d_out: int | None = None, d_in: int | None = None,
+                  dtype=torch.bfloat16):
+    """[d_out, d_in] float32 or bf16 values of a packed weight (defaults: every row and column
+    that the tiles hold)."""
+    dev = _lead(codes, "codes", 3)
+    kind = _code(_PLAIN, dtype, "dtype")
+    K = codes.shape[1] * 128 if d_in is None else d_in
+    N, group, c, s, z = _packed(codes, scales, zeros, K, d_out, dev)
+    out = torch.empty((N, K), dtype=dtype, device=codes.device)
+    _call("w4_dequantize", dev, c, s, z, N, K, group, kind, out.data_ptr())
+    return out
+
+
+def _x_args(x, x_scale, dtype):
+    dev = _lead(x, "x", 2)
+    return dev, _code(_X, x.dtype, "x"), _like(x_scale, "x_scale", dev, torch.float32, (x.shape[0],)), \
+        _code(_PLAIN, dtype, "dtype")
+
+
+def w4_matvec(x, codes, scales, zeros=None, *, d_out: int | None = None, x_scale=None, dtype=torch.bfloat16,
+              out=None):
+    """y = (x_scale x) W^T [T, d_out] in dtype (float32 or bf16) for x [T, d_in] bf16, float8_e4m3fn
+    or int8 and a packed weight; x_scale: float32 [T] or None. Made for up to 64 rows."""
+    dev, xt, xs, yt = _x_args(x, x_scale, dtype)
+    T, K = x.shape
+    N, group, c, s, z = _packed(codes, scales, zeros, K, d_out, dev)
+    if out is None:
+        out = torch.empty((T, N), dtype=dtype, device=x.device)
+    _call("w4_matvec", dev, T, K, N, group, xt, x.data_ptr(), xs, c, s, z, yt, _like(out, "out", dev, dtype, (T, N)))
+    return out
+
+
+def w4_matvec_multi(x, codes, scales, zeros=None, *, d_out=None, x_scale=None, dtype=torch.bfloat16):
+    """[y_g] of several packed weights (lists, one entry per weight) that read the same x, in one
+    launch: the same values as one w4_matvec each. zeros: None, or one entry per weight."""
+    dev, xt, xs, yt = _x_args(x, x_scale, dtype)
+    T, K = x.shape
+    n = len(codes)
+    if not 1 <= n <= LN_MAX_PROJ or len(scales) != n or (zeros is not None and len(zeros) != n) or \
+            (d_out is not None and len(d_out) != n):
+        raise ValueError(f"codes, scales (zeros, d_out) must be lists of the same length, 1 to {LN_MAX_PROJ}")
+    ws = [_packed(codes[g], scales[g], None if zeros is None else zeros[g], K, None if d_out is None else d_out[g],
+                  dev, f"[{g}]") for g in range(n)]
+    if any(w[1] != ws[0][1] for w in ws):
+        raise ValueError("all weights must share the group size")
+    if any((w[4] is None) != (ws[0][4] is None) for w in ws):
+        raise ValueError("zeros must be given for every weight or for none")
+    ys = [torch.empty((T, w[0]), dtype=dtype, device=x.device) for w in ws]
+    arr = _p * n
+    _call("w4_matvec_multi", dev, T, K, n, (_i64 * n)(*(w[0] for w in ws)), ws[0][1], xt, x.data_ptr(), xs,
+          arr(*(w[2] for w in ws)), arr(*(w[3] for w in ws)),
+          None if ws[0][4] is None else arr(*(w[4] for w in ws)), yt, arr(*(y.data_ptr() for y in ys)))
+    return ys
