@@ -3,149 +3,560 @@
 //     h = round(x + res), rstd = 1 / sqrt(mean(h^2) + eps), y = h rstd w
 //     dx = dh + rstd (g - n mean(g n)),  dw = sum_t dy n,  g = dy w, n = h rstd
 //
-// One workgroup per row; every sum in float32.
+// Bound by HBM: every operand is read once and every result written once. A row stays
+// in registers between its reduction and its output: TPR threads hold it, NV 16-byte
+// vectors each (thread i: vectors i, i + TPR, ...), so all loads of a row are in flight
+// together. The 8-bit scale needs max |h w| rstd, which the same reduction finds. All
+// statistics and sums are float32.
+//
+// Rows need not be 16-byte aligned (d of any size): vectors are loaded with the
+// alignment of an element, which the hardware allows for global memory, and only the
+// last, partial vector of a row goes element by element.
+#include <algorithm>
+#include <type_traits>
+
 #include "device_common.h"
 #include "norm_w4_launch.h"
 
 namespace lnf4 {
 namespace {
 
-constexpr int kThreads = 256;
+template <typename E>
+struct Vec;
+template <>
+struct Vec<uint16_t> {
+  static constexpr int kN = 8;
+};
+template <>
+struct Vec<float> {
+  static constexpr int kN = 4;
+};
 
-__device__ __forceinline__ float load1(const float* p, int64_t i) { return p[i]; }
-__device__ __forceinline__ float load1(const uint16_t* p, int64_t i) { return bf16_to_f32(p[i]); }
-__device__ __forceinline__ void store1(float* p, int64_t i, float v) { p[i] = v; }
-__device__ __forceinline__ void store1(uint16_t* p, int64_t i, float v) { p[i] = to_bf16(v); }
-__device__ __forceinline__ float round_to(const float*, float v) { return v; }
-__device__ __forceinline__ float round_to(const uint16_t*, float v) { return bf16_to_f32(to_bf16(v)); }
+// 16 bytes with the alignment of their elements.
+template <typename E>
+struct Raw;
+template <>
+struct Raw<uint16_t> {
+  typedef uint32_t type __attribute__((ext_vector_type(4), aligned(2)));
+};
+template <>
+struct Raw<float> {
+  typedef uint32_t type __attribute__((ext_vector_type(4), aligned(4)));
+};
+typedef uint32_t raw8_t __attribute__((ext_vector_type(2), aligned(1)));
 
-// Sum and maximum over the workgroup, the same in every thread.
-__device__ __forceinline__ void block_sum_max(float& s, float& m, float (*red)[kThreads / 64]) {
+__device__ __forceinline__ float to_f32(uint16_t v) { return bf16_to_f32(v); }
+__device__ __forceinline__ float to_f32(float v) { return v; }
+template <typename E>
+__device__ __forceinline__ E from_f32(float v);
+template <>
+__device__ __forceinline__ uint16_t from_f32<uint16_t>(float v) {
+  return to_bf16(v);
+}
+template <>
+__device__ __forceinline__ float from_f32<float>(float v) {
+  return v;
+}
+
+// A vector of a row as it lies in memory; elements past the row's end are zero.
+template <typename E>
+struct Held {
+  uint32_t u[4];
+};
+template <typename E>
+__device__ __forceinline__ Held<E> load_vec(const E* p, int left) {
+  constexpr int kN = Vec<E>::kN;
+  Held<E> o{{0u, 0u, 0u, 0u}};
+  if (left >= kN) {
+    const auto v = *reinterpret_cast<const typename Raw<E>::type*>(p);
+    o.u[0] = v.x, o.u[1] = v.y, o.u[2] = v.z, o.u[3] = v.w;
+  } else if (left > 0) {
+#pragma unroll
+    for (int j = 0; j < kN; ++j)
+      if (j < left) {
+        if constexpr (sizeof(E) == 4) o.u[j] = __float_as_uint(p[j]);
+        else o.u[j / 2] |= static_cast<uint32_t>(p[j]) << (16 * (j & 1));
+      }
+  }
+  return o;
+}
+template <typename E>
+__device__ __forceinline__ float elem(const Held<E>& v, int j) {
+  if constexpr (sizeof(E) == 4) return __uint_as_float(v.u[j]);
+  else return __uint_as_float((j & 1) ? (v.u[j / 2] & 0xFFFF0000u) : (v.u[j / 2] << 16));
+}
+template <typename E>
+__device__ __forceinline__ Held<E> hold(const float (&f)[Vec<E>::kN]) {
+  Held<E> o;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if constexpr (sizeof(E) == 4) o.u[j] = __float_as_uint(f[j]);
+    else o.u[j] = pack_bf16x2(f[2 * j], f[2 * j + 1]);
+  }
+  return o;
+}
+template <typename E>
+__device__ __forceinline__ void store_vec(E* p, int left, const Held<E>& v) {
+  constexpr int kN = Vec<E>::kN;
+  if (left >= kN) {
+    *reinterpret_cast<typename Raw<E>::type*>(p) = typename Raw<E>::type{v.u[0], v.u[1], v.u[2], v.u[3]};
+  } else {
+#pragma unroll
+    for (int j = 0; j < kN; ++j)
+      if (j < left) p[j] = from_f32<E>(elem(v, j));
+  }
+}
+
+// 8-bit levels of four values (byte j = value j); |v| is at most the format's largest
+// up to a float32 rounding.
+template <int OUT>
+__device__ __forceinline__ uint32_t levels4(const float* v) {
+  if constexpr (OUT == kRowE4m3) {
+    int w = __builtin_amdgcn_cvt_pk_fp8_f32(v[0], v[1], 0, false);
+    return static_cast<uint32_t>(__builtin_amdgcn_cvt_pk_fp8_f32(v[2], v[3], w, true));
+  } else {
+    uint32_t w = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      w |= (static_cast<uint32_t>(static_cast<int>(__builtin_rintf(v[j]))) & 0xFFu) << (8 * j);
+    return w;
+  }
+}
+
+// The values as packed, not as unpacked for the reduction, stay in registers after it
+// (the compiler would keep both: twice the registers, half the rows in flight).
+template <typename E>
+__device__ __forceinline__ void repack(Held<E>& v) {
+  if constexpr (sizeof(E) == 2) asm volatile("" : "+v"(v.u[0]), "+v"(v.u[1]), "+v"(v.u[2]), "+v"(v.u[3]));
+}
+
+// Sum and maximum over the TPR threads of a row, the same bits in each. The threads of
+// a row are consecutive; red has a pair per wave of the workgroup.
+template <int TPR>
+__device__ __forceinline__ void row_reduce(float& s, float& m, float2* red) {
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) {
     s += __shfl_xor(s, o);
     m = fmaxf(m, __shfl_xor(m, o));
   }
-  if ((threadIdx.x & 63) == 0) {
-    red[0][threadIdx.x >> 6] = s;
-    red[1][threadIdx.x >> 6] = m;
+  if constexpr (TPR > 64) {
+    constexpr int kWaves = TPR / 64;
+    const int wave = threadIdx.x >> 6;
+    if ((threadIdx.x & 63) == 0) red[wave] = make_float2(s, m);
+    __syncthreads();
+    const float2* r = red + wave / kWaves * kWaves;
+    s = 0.f;
+#pragma unroll
+    for (int i = 0; i < kWaves; ++i) {
+      s += r[i].x;
+      m = fmaxf(m, r[i].y);
+    }
   }
-  __syncthreads();
-  s = red[0][0] + red[0][1] + red[0][2] + red[0][3];
-  m = fmaxf(fmaxf(red[1][0], red[1][1]), fmaxf(red[1][2], red[1][3]));
 }
 
-__device__ __forceinline__ uint8_t to_e4m3(float v) {
-  return static_cast<uint8_t>(__builtin_amdgcn_cvt_pk_fp8_f32(v, v, 0, false) & 0xFF);
-}
-__device__ __forceinline__ uint8_t to_i8(float v) {
-  return static_cast<uint8_t>(static_cast<int>(__builtin_rintf(fminf(fmaxf(v, -127.f), 127.f))));
+constexpr float kTiny = 0x1p-100f, kUp = 0x1p64f;
+
+// ---- forward ---------------------------------------------------------------------------
+template <typename E, int OUT, int TPR, int NV>
+__global__ __launch_bounds__((TPR < 256 ? 256 : TPR)) void rmsnorm_fwd_kernel(
+    int64_t T, int d, float eps, const E* __restrict__ x, const E* __restrict__ res, const E* __restrict__ w,
+    E* __restrict__ h, void* __restrict__ y, float* __restrict__ q_scale, float* __restrict__ rstd_out) {
+  constexpr int kN = Vec<E>::kN, kBlock = TPR < 256 ? 256 : TPR;
+  constexpr bool kQuant = OUT == kRowE4m3 || OUT == kRowI8;
+  __shared__ float2 red[kBlock / 64];
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * (kBlock / TPR) + threadIdx.x / TPR;
+  const int i0 = threadIdx.x % TPR;
+  if (TPR < 256 && t >= T) return;  // (whole waves; no barrier follows at TPR = 64)
+  const int64_t row = t * d;
+  Held<E> hv[NV], wv[NV];
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    const int at = (i0 + v * TPR) * kN;
+    hv[v] = load_vec(x + row + at, d - at);
+  }
+  if (res != nullptr) {
+    Held<E> rv[NV];
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int at = (i0 + v * TPR) * kN;
+      rv[v] = load_vec(res + row + at, d - at);
+    }
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int at = (i0 + v * TPR) * kN;
+      wv[v] = load_vec(w + at, d - at);
+    }
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int at = (i0 + v * TPR) * kN;
+      float f[kN];
+#pragma unroll
+      for (int j = 0; j < kN; ++j) f[j] = elem(hv[v], j) + elem(rv[v], j);
+      hv[v] = hold<E>(f);
+      store_vec(h + row + at, d - at, hv[v]);
+    }
+  } else {
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int at = (i0 + v * TPR) * kN;
+      wv[v] = load_vec(w + at, d - at);
+    }
+  }
+  float s = 0.f, m = 0.f;
+#pragma unroll
+  for (int v = 0; v < NV; ++v)
+#pragma unroll
+    for (int j = 0; j < kN; ++j) {
+      const float f = elem(hv[v], j);
+      s += f * f;
+      if constexpr (kQuant) m = fmaxf(m, fabsf(f * elem(wv[v], j)));
+    }
+  row_reduce<TPR>(s, m, red);
+  const float rstd = 1.0f / __builtin_sqrtf(s / static_cast<float>(d) + eps);
+  if (i0 == 0 && rstd_out != nullptr) rstd_out[t] = rstd;
+  float up = 1.f, inv = 0.f;
+  if constexpr (kQuant) {
+    constexpr float kTop = OUT == kRowE4m3 ? 448.f : 127.f;
+    const float top = m * rstd, scale = top / kTop;
+    // levels are y times one reciprocal a row; rows so small that it would overflow are
+    // scaled up first (exactly)
+    up = top < kTiny ? kUp : 1.f;
+    inv = scale > 0.f ? kTop / (top * up) : 0.f;
+    if (i0 == 0) q_scale[t] = scale;
+  }
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    const int at = (i0 + v * TPR) * kN, left = d - at;
+    repack(hv[v]);
+    repack(wv[v]);
+    float f[kN];
+#pragma unroll
+    for (int j = 0; j < kN; ++j) f[j] = elem(hv[v], j) * rstd * elem(wv[v], j);
+    if constexpr (kQuant) {
+#pragma unroll
+      for (int j = 0; j < kN; ++j) f[j] = f[j] * up * inv;
+      uint32_t lv[kN / 4];
+#pragma unroll
+      for (int j = 0; j < kN / 4; ++j) lv[j] = levels4<OUT>(f + 4 * j);
+      uint8_t* p = static_cast<uint8_t*>(y) + row + at;
+      if (left >= kN) {
+        if constexpr (kN == 8) *reinterpret_cast<raw8_t*>(p) = raw8_t{lv[0], lv[1]};
+        else __builtin_memcpy(p, lv, 4);
+      } else {
+#pragma unroll
+        for (int j = 0; j < kN; ++j)
+          if (j < left) p[j] = static_cast<uint8_t>(lv[j / 4] >> (8 * (j & 3)));
+      }
+    } else if (left > 0) {
+      store_vec(static_cast<E*>(y) + row + at, left, hold<E>(f));
+    }
+  }
 }
 
+// Rows wider than the registers of a workgroup hold: the row is read twice, the second
+// time mostly from L2 (h is formed again from x and the residual).
+constexpr int kLoop = 1024;
 template <typename E, int OUT>
-__global__ __launch_bounds__(kThreads) void rmsnorm_fwd_kernel(int d, float eps, const E* __restrict__ x,
-                                                               const E* __restrict__ res, const E* __restrict__ w,
-                                                               E* __restrict__ h, void* __restrict__ y,
-                                                               float* __restrict__ q_scale,
-                                                               float* __restrict__ rstd_out) {
-  __shared__ float red[2][kThreads / 64];
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * d;
+__global__ __launch_bounds__(kLoop) void rmsnorm_fwd_loop_kernel(int d, float eps, const E* __restrict__ x,
+                                                                 const E* __restrict__ res,
+                                                                 const E* __restrict__ w, E* __restrict__ h,
+                                                                 void* __restrict__ y,
+                                                                 float* __restrict__ q_scale,
+                                                                 float* __restrict__ rstd_out) {
+  __shared__ float2 red[kLoop / 64];
+  const int64_t t = blockIdx.x, row = t * d;
   auto h_at = [&](int i) {
-    const float v = load1(x, row + i);
-    return res == nullptr ? v : round_to(x, v + load1(res, row + i));
+    const float v = to_f32(x[row + i]);
+    return res == nullptr ? v : to_f32(from_f32<E>(v + to_f32(res[row + i])));
   };
   float s = 0.f, m = 0.f;
-  for (int i = threadIdx.x; i < d; i += kThreads) {
+  for (int i = threadIdx.x; i < d; i += kLoop) {
     const float v = h_at(i);
     s += v * v;
-    m = fmaxf(m, fabsf(v * load1(w, i)));
+    m = fmaxf(m, fabsf(v * to_f32(w[i])));
   }
-  block_sum_max(s, m, red);
+  row_reduce<kLoop>(s, m, red);
   const float rstd = 1.0f / __builtin_sqrtf(s / static_cast<float>(d) + eps);
-  const float scale = m * rstd / (OUT == kRowE4m3 ? 448.f : 127.f);
-  for (int i = threadIdx.x; i < d; i += kThreads) {
+  constexpr float kTop = OUT == kRowE4m3 ? 448.f : 127.f;
+  const float top = m * rstd, scale = top / kTop, up = top < kTiny ? kUp : 1.f;
+  const float inv = scale > 0.f ? kTop / (top * up) : 0.f;
+  for (int i = threadIdx.x; i < d; i += kLoop) {
     const float v = h_at(i);
-    if (res != nullptr) store1(h, row + i, v);
-    const float o = v * rstd * load1(w, i);
-    if constexpr (OUT == kRowE4m3)
-      static_cast<uint8_t*>(y)[row + i] = scale > 0.f ? to_e4m3(o / scale) : 0;
-    else if constexpr (OUT == kRowI8)
-      static_cast<uint8_t*>(y)[row + i] = scale > 0.f ? to_i8(o / scale) : 0;
-    else
-      store1(static_cast<E*>(y), row + i, o);
+    if (res != nullptr) h[row + i] = from_f32<E>(v);
+    const float o = v * rstd * to_f32(w[i]);
+    if constexpr (OUT == kRowE4m3 || OUT == kRowI8) {
+      const float f[4] = {o * up * inv, 0.f, 0.f, 0.f};
+      static_cast<uint8_t*>(y)[row + i] = static_cast<uint8_t>(levels4<OUT>(f));
+    } else {
+      static_cast<E*>(y)[row + i] = from_f32<E>(o);
+    }
   }
   if (threadIdx.x == 0) {
-    if (rstd_out != nullptr) rstd_out[blockIdx.x] = rstd;
-    if (OUT == kRowE4m3 || OUT == kRowI8) q_scale[blockIdx.x] = scale;
+    if (rstd_out != nullptr) rstd_out[t] = rstd;
+    if (OUT == kRowE4m3 || OUT == kRowI8) q_scale[t] = scale;
   }
 }
 
+// ---- backward --------------------------------------------------------------------------
+// BLOCK / TPR rows at a time (the workgroup's slots), the workgroup strides over all
+// rows; with DW every thread also sums dy n of its columns over its rows, the slots'
+// sums are added in LDS in a fixed order, and part[workgroup][d] holds the result.
+template <typename E, int TPR, int NV, int BLOCK, bool DW>
+__global__ __launch_bounds__(BLOCK) void rmsnorm_bwd_kernel(int64_t T, int d, const E* __restrict__ dy,
+                                                            const E* __restrict__ dh, const E* __restrict__ h,
+                                                            const E* __restrict__ w,
+                                                            const float* __restrict__ rstd_in,
+                                                            E* __restrict__ dx, float* __restrict__ part) {
+  constexpr int kN = Vec<E>::kN, kSlots = BLOCK / TPR;
+  __shared__ float2 red[BLOCK / 64];
+  const int i0 = threadIdx.x % TPR, slot = threadIdx.x / TPR;
+  Held<E> wv[NV];
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    const int at = (i0 + v * TPR) * kN;
+    wv[v] = load_vec(w + at, d - at);
+  }
+  float acc[DW ? NV * kN : 1];
+#pragma unroll
+  for (int j = 0; j < (DW ? NV * kN : 1); ++j) acc[j] = 0.f;
+  // every slot runs as often as the workgroup's first (barriers); one past the end has
+  // vectors of length 0: it loads zeros and stores nothing
+  for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * kSlots; t0 < T; t0 += static_cast<int64_t>(gridDim.x) * kSlots) {
+    const bool ok = t0 + slot < T;
+    const int64_t t = ok ? t0 + slot : t0;
+    const int64_t row = t * d;
+    const int dd = ok ? d : 0;
+    Held<E> hv[NV], gv[NV];
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int at = (i0 + v * TPR) * kN;
+      hv[v] = load_vec(h + row + at, dd - at);
+      gv[v] = load_vec(dy + row + at, dd - at);
+    }
+    const float rstd = rstd_in[t];
+    float s = 0.f, unused = 0.f;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      repack(wv[v]);
+#pragma unroll
+      for (int j = 0; j < kN; ++j) {
+        const float n = elem(hv[v], j) * rstd, g = elem(gv[v], j);
+        if constexpr (DW) acc[v * kN + j] += g * n;
+        s += g * elem(wv[v], j) * n;
+      }
+    }
+    if constexpr (TPR > 64) __syncthreads();  // the last row's red has been read
+    row_reduce<TPR>(s, unused, red);
+    const float c = s / static_cast<float>(d);
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int at = (i0 + v * TPR) * kN, left = dd - at;
+      repack(hv[v]);
+      repack(gv[v]);
+      repack(wv[v]);
+      float f[kN];
+#pragma unroll
+      for (int j = 0; j < kN; ++j) {
+        const float n = elem(hv[v], j) * rstd;
+        f[j] = rstd * (elem(gv[v], j) * elem(wv[v], j) - n * c);
+      }
+      if (dh != nullptr) {
+        const Held<E> e = load_vec(dh + row + at, left);
+#pragma unroll
+        for (int j = 0; j < kN; ++j) f[j] += elem(e, j);
+      }
+      if (left > 0) store_vec(dx + row + at, left, hold<E>(f));
+    }
+  }
+  if constexpr (DW) {
+    float* out = part + static_cast<int64_t>(blockIdx.x) * d;
+    if constexpr (kSlots > 1) {
+      __shared__ float sum[NV * TPR * kN];  // [v][j][thread]: lanes side by side, no bank conflicts
+      for (int k = 0; k < kSlots; ++k) {
+        if (slot == k) {
+#pragma unroll
+          for (int v = 0; v < NV; ++v)
+#pragma unroll
+            for (int j = 0; j < kN; ++j) {
+              float* p = sum + (v * kN + j) * TPR + i0;
+              *p = k == 0 ? acc[v * kN + j] : *p + acc[v * kN + j];
+            }
+        }
+        __syncthreads();
+      }
+      for (int i = threadIdx.x; i < d; i += BLOCK) {
+        const int vec = i / kN;
+        out[i] = sum[(vec / TPR * kN + i % kN) * TPR + vec % TPR];
+      }
+    } else {
+#pragma unroll
+      for (int v = 0; v < NV; ++v)
+#pragma unroll
+        for (int j = 0; j < kN; ++j) {
+          const int i = (i0 + v * TPR) * kN + j;
+          if (i < d) out[i] = acc[v * kN + j];
+        }
+    }
+  }
+}
+
+// Rows wider than the registers hold: read twice.
 template <typename E>
-__global__ __launch_bounds__(kThreads) void rmsnorm_bwd_kernel(int d, const E* __restrict__ dy,
-                                                               const E* __restrict__ dh, const E* __restrict__ h,
-                                                               const E* __restrict__ w,
-                                                               const float* __restrict__ rstd_in,
-                                                               E* __restrict__ dx) {
-  __shared__ float red[2][kThreads / 64];
+__global__ __launch_bounds__(kLoop) void rmsnorm_bwd_loop_kernel(int d, const E* __restrict__ dy,
+                                                                 const E* __restrict__ dh,
+                                                                 const E* __restrict__ h, const E* __restrict__ w,
+                                                                 const float* __restrict__ rstd_in,
+                                                                 E* __restrict__ dx) {
+  __shared__ float2 red[kLoop / 64];
   const int64_t row = static_cast<int64_t>(blockIdx.x) * d;
   const float rstd = rstd_in[blockIdx.x];
-  float s = 0.f, m = 0.f;
-  for (int i = threadIdx.x; i < d; i += kThreads)
-    s += load1(dy, row + i) * load1(w, i) * (load1(h, row + i) * rstd);
-  block_sum_max(s, m, red);
+  float s = 0.f, unused = 0.f;
+  for (int i = threadIdx.x; i < d; i += kLoop)
+    s += to_f32(dy[row + i]) * to_f32(w[i]) * (to_f32(h[row + i]) * rstd);
+  row_reduce<kLoop>(s, unused, red);
   const float c = s / static_cast<float>(d);
-  for (int i = threadIdx.x; i < d; i += kThreads) {
-    const float g = load1(dy, row + i) * load1(w, i), n = load1(h, row + i) * rstd;
-    const float v = rstd * (g - n * c);
-    store1(dx, row + i, dh == nullptr ? v : v + load1(dh, row + i));
+  for (int i = threadIdx.x; i < d; i += kLoop) {
+    float f = rstd * (to_f32(dy[row + i]) * to_f32(w[i]) - to_f32(h[row + i]) * rstd * c);
+    if (dh != nullptr) f += to_f32(dh[row + i]);
+    dx[row + i] = from_f32<E>(f);
   }
 }
 
-// One thread per column; consecutive rows are summed in float32 partials of 64 rows.
+// part[b][i] = sum of dy n over the rows b, b + blocks, ... of column i.
 template <typename E>
-__global__ __launch_bounds__(kThreads) void rmsnorm_dw_kernel(int64_t T, int d, const E* __restrict__ dy,
+__global__ __launch_bounds__(256) void rmsnorm_dw_part_kernel(int64_t T, int d, const E* __restrict__ dy,
                                                               const E* __restrict__ h,
-                                                              const float* __restrict__ rstd, E* __restrict__ dw) {
-  const int i = blockIdx.x * kThreads + threadIdx.x;
+                                                              const float* __restrict__ rstd,
+                                                              float* __restrict__ part) {
+  const int i = blockIdx.x * 256 + threadIdx.x;
   if (i >= d) return;
-  float total = 0.f;
-  for (int64_t t0 = 0; t0 < T; t0 += 64) {
-    float s = 0.f;
-    for (int64_t t = t0; t < T && t < t0 + 64; ++t) s += load1(dy, t * d + i) * (load1(h, t * d + i) * rstd[t]);
-    total += s;
+  float s = 0.f;
+  for (int64_t t = blockIdx.y; t < T; t += gridDim.y) s += to_f32(dy[t * d + i]) * (to_f32(h[t * d + i]) * rstd[t]);
+  part[static_cast<int64_t>(blockIdx.y) * d + i] = s;
+}
+
+// dw[i] = sum over blocks of part[block][i]: 32 columns a workgroup, 32 threads a
+// column over the blocks, joined in LDS in a fixed order.
+template <typename E>
+__global__ __launch_bounds__(1024) void rmsnorm_dw_kernel(int blocks, int d, const float* __restrict__ part,
+                                                          E* __restrict__ dw) {
+  __shared__ float red[32][33];
+  const int c = threadIdx.x & 31, k = threadIdx.x >> 5, i = blockIdx.x * 32 + c;
+  float s = 0.f;
+  if (i < d)
+    for (int b = k; b < blocks; b += 32) s += part[static_cast<int64_t>(b) * d + i];
+  red[k][c] = s;
+  __syncthreads();
+  if (k == 0 && i < d) {
+    float v = 0.f;
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v += red[j][c];
+    dw[i] = from_f32<E>(v);
   }
-  store1(dw, i, total);
 }
 
 template <typename E>
-__global__ __launch_bounds__(kThreads) void zero_kernel(E* __restrict__ p, int64_t n) {
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
+__global__ __launch_bounds__(256) void zero_kernel(E* __restrict__ p, int64_t n) {
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
   if (i < n) p[i] = E(0);
 }
 
-template <typename E>
-hipError_t fwd(int64_t T, int d, float eps, const void* x, const void* res, const void* w, void* h, int out, void* y,
+// Threads and vectors a thread of a row of `vecs` vectors. Many rows: one wave a row (no
+// barrier) up to `most` vectors a lane, then 4 waves, then 16. Few rows leave the GPU idle
+// whatever is chosen, so a row takes as many threads as have a vector: fewer loads one
+// after another on the path from the first load to the last store.
+constexpr int kFewRows = 512;
+struct RowShape {
+  int tpr, nv;  // tpr 0: does not fit
+};
+RowShape row_shape(int64_t T, int64_t vecs, int most) {
+  const int nv64 = static_cast<int>((vecs + 63) / 64), nv256 = static_cast<int>((vecs + 255) / 256);
+  const int nv1024 = static_cast<int>((vecs + 1023) / 1024);
+  auto up = [](int n) { return n <= 1 ? 1 : n <= 2 ? 2 : 4; };
+  if (nv64 == 1 || (T > kFewRows && nv64 <= most)) return {64, up(nv64)};
+  if (nv256 == 1 || (T > kFewRows && nv256 <= most)) return {256, up(nv256)};
+  if (nv1024 <= 4) return {1024, up(nv1024)};
+  return {0, 0};
+}
+
+template <typename E, int OUT>
+hipError_t fwd(int64_t T, int d, float eps, const void* xv, const void* rv, const void* wv, void* hv, void* y,
                float* q_scale, float* rstd, hipStream_t stream) {
-  const auto xe = static_cast<const E*>(x), re = static_cast<const E*>(res), we = static_cast<const E*>(w);
-  const dim3 grid(static_cast<unsigned>(T));
-  if (out == kRowE4m3)
-    rmsnorm_fwd_kernel<E, kRowE4m3><<<grid, kThreads, 0, stream>>>(d, eps, xe, re, we, static_cast<E*>(h), y, q_scale, rstd);
-  else if (out == kRowI8)
-    rmsnorm_fwd_kernel<E, kRowI8><<<grid, kThreads, 0, stream>>>(d, eps, xe, re, we, static_cast<E*>(h), y, q_scale, rstd);
+  const auto x = static_cast<const E*>(xv), res = static_cast<const E*>(rv), w = static_cast<const E*>(wv);
+  const auto h = static_cast<E*>(hv);
+  const RowShape sh = row_shape(T, (d + Vec<E>::kN - 1) / Vec<E>::kN, 4);
+  auto go = [&](auto tpr, auto nv) {
+    constexpr int kTpr = decltype(tpr)::value, kNv = decltype(nv)::value, kRows = kTpr < 256 ? 256 / kTpr : 1;
+    rmsnorm_fwd_kernel<E, OUT, kTpr, kNv><<<dim3(static_cast<unsigned>((T + kRows - 1) / kRows)), kTpr * kRows, 0, stream>>>(
+        T, d, eps, x, res, w, h, y, q_scale, rstd);
+  };
+  auto pick = [&](auto tpr) {
+    switch (sh.nv) {
+      case 1: go(tpr, std::integral_constant<int, 1>{}); break;
+      case 2: go(tpr, std::integral_constant<int, 2>{}); break;
+      default: go(tpr, std::integral_constant<int, 4>{}); break;
+    }
+  };
+  if (sh.tpr == 64) pick(std::integral_constant<int, 64>{});
+  else if (sh.tpr == 256) pick(std::integral_constant<int, 256>{});
+  else if (sh.tpr == 1024) pick(std::integral_constant<int, 1024>{});
   else
-    rmsnorm_fwd_kernel<E, kRowF32><<<grid, kThreads, 0, stream>>>(d, eps, xe, re, we, static_cast<E*>(h), y, q_scale, rstd);
+    rmsnorm_fwd_loop_kernel<E, OUT><<<dim3(static_cast<unsigned>(T)), kLoop, 0, stream>>>(d, eps, x, res, w, h, y,
+                                                                                          q_scale, rstd);
   return hipGetLastError();
 }
 
 template <typename E>
-hipError_t bwd(int64_t T, int d, const void* dy, const void* dh, const void* h, const void* w, const float* rstd,
-               void* dx, void* dw, hipStream_t stream) {
-  const auto dye = static_cast<const E*>(dy), he = static_cast<const E*>(h);
-  rmsnorm_bwd_kernel<E><<<dim3(static_cast<unsigned>(T)), kThreads, 0, stream>>>(
-      d, dye, static_cast<const E*>(dh), he, static_cast<const E*>(w), rstd, static_cast<E*>(dx));
-  if (dw != nullptr)
-    rmsnorm_dw_kernel<E><<<dim3((d + kThreads - 1) / kThreads), kThreads, 0, stream>>>(T, d, dye, he, rstd,
-                                                                                      static_cast<E*>(dw));
+hipError_t fwd_out(int64_t T, int d, float eps, const void* x, const void* res, const void* w, void* h, int out,
+                   void* y, float* q_scale, float* rstd, hipStream_t stream) {
+  if (out == kRowE4m3) return fwd<E, kRowE4m3>(T, d, eps, x, res, w, h, y, q_scale, rstd, stream);
+  if (out == kRowI8) return fwd<E, kRowI8>(T, d, eps, x, res, w, h, y, q_scale, rstd, stream);
+  return fwd<E, kRowF32>(T, d, eps, x, res, w, h, y, q_scale, rstd, stream);  // E itself
+}
+
+// Workgroups of the backward, each with one row of float32 partial sums of dw: two or
+// more a CU, few enough that the partial sums stay small beside the rows.
+constexpr int kBwdBlocks = 512;
+constexpr int kBwdThreads = 512;
+int bwd_blocks(int64_t T) { return static_cast<int>(T < kBwdBlocks ? T : kBwdBlocks); }
+
+template <typename E>
+hipError_t bwd(int64_t T, int d, const void* dyv, const void* dhv, const void* hv, const void* wv, const float* rstd,
+               void* dxv, void* dwv, void* workspace, hipStream_t stream) {
+  const auto dy = static_cast<const E*>(dyv), dh = static_cast<const E*>(dhv), h = static_cast<const E*>(hv);
+  const auto w = static_cast<const E*>(wv);
+  const auto dx = static_cast<E*>(dxv), dw = static_cast<E*>(dwv);
+  const auto part = static_cast<float*>(workspace);
+  // (dw's sums take a register an element: 16 elements a thread leave four waves a SIMD)
+  const RowShape sh = row_shape(T, (d + Vec<E>::kN - 1) / Vec<E>::kN, dw != nullptr ? 16 / Vec<E>::kN : 4);
+  int blocks = bwd_blocks(T);
+  auto go = [&](auto tpr, auto nv) {
+    constexpr int kTpr = decltype(tpr)::value, kNv = decltype(nv)::value;
+    constexpr int kBlock = kTpr < kBwdThreads ? kBwdThreads : kTpr, kSlots = kBlock / kTpr;
+    blocks = static_cast<int>(std::min<int64_t>((T + kSlots - 1) / kSlots, blocks));
+    if (dw != nullptr)
+      rmsnorm_bwd_kernel<E, kTpr, kNv, kBlock, true><<<dim3(blocks), kBlock, 0, stream>>>(T, d, dy, dh, h, w, rstd, dx, part);
+    else
+      rmsnorm_bwd_kernel<E, kTpr, kNv, kBlock, false><<<dim3(blocks), kBlock, 0, stream>>>(T, d, dy, dh, h, w, rstd, dx, part);
+  };
+  auto pick = [&](auto tpr) {
+    switch (sh.nv) {
+      case 1: go(tpr, std::integral_constant<int, 1>{}); break;
+      case 2: go(tpr, std::integral_constant<int, 2>{}); break;
+      default: go(tpr, std::integral_constant<int, 4>{}); break;
+    }
+  };
+  if (sh.tpr == 64) pick(std::integral_constant<int, 64>{});
+  else if (sh.tpr == 256) pick(std::integral_constant<int, 256>{});
+  else if (sh.tpr == 1024) pick(std::integral_constant<int, 1024>{});
+  else {
+    rmsnorm_bwd_loop_kernel<E><<<dim3(static_cast<unsigned>(T)), kLoop, 0, stream>>>(d, dy, dh, h, w, rstd, dx);
+    if (dw != nullptr) {
+      blocks = std::min(blocks, 64);
+      rmsnorm_dw_part_kernel<E><<<dim3((d + 255) / 256, blocks), 256, 0, stream>>>(T, d, dy, h, rstd, part);
+    }
+  }
+  if (dw != nullptr) rmsnorm_dw_kernel<E><<<dim3((d + 31) / 32), 1024, 0, stream>>>(blocks, d, part, dw);
   return hipGetLastError();
 }
 
@@ -154,22 +565,25 @@ hipError_t bwd(int64_t T, int d, const void* dy, const void* dh, const void* h, 
 hipError_t launch_rmsnorm_fwd(int64_t T, int d, int dtype, float eps, const void* x, const void* residual,
                               const void* w, void* h, int out, void* y, float* q_scale, float* rstd,
                               hipStream_t stream) {
-  return dtype == kRowBf16 ? fwd<uint16_t>(T, d, eps, x, residual, w, h, out, y, q_scale, rstd, stream)
-                           : fwd<float>(T, d, eps, x, residual, w, h, out, y, q_scale, rstd, stream);
+  return dtype == kRowBf16 ? fwd_out<uint16_t>(T, d, eps, x, residual, w, h, out, y, q_scale, rstd, stream)
+                           : fwd_out<float>(T, d, eps, x, residual, w, h, out, y, q_scale, rstd, stream);
 }
 
-size_t rmsnorm_bwd_bytes(int64_t, int64_t) { return 0; }
+size_t rmsnorm_bwd_bytes(int64_t T, int64_t d) {
+  return (static_cast<size_t>(bwd_blocks(T)) * d * 4 + 255) / 256 * 256;
+}
 
 hipError_t launch_rmsnorm_bwd(int64_t T, int d, int dtype, const void* dy, const void* dh, const void* h,
-                              const void* w, const float* rstd, void* dx, void* dw, void*, hipStream_t stream) {
-  return dtype == kRowBf16 ? bwd<uint16_t>(T, d, dy, dh, h, w, rstd, dx, dw, stream)
-                           : bwd<float>(T, d, dy, dh, h, w, rstd, dx, dw, stream);
+                              const void* w, const float* rstd, void* dx, void* dw, void* workspace,
+                              hipStream_t stream) {
+  return dtype == kRowBf16 ? bwd<uint16_t>(T, d, dy, dh, h, w, rstd, dx, dw, workspace, stream)
+                           : bwd<float>(T, d, dy, dh, h, w, rstd, dx, dw, workspace, stream);
 }
 
 hipError_t launch_zero(void* p, int64_t n, int dtype, hipStream_t stream) {
-  const dim3 grid(static_cast<unsigned>((n + kThreads - 1) / kThreads));
-  if (dtype == kRowBf16) zero_kernel<<<grid, kThreads, 0, stream>>>(static_cast<uint16_t*>(p), n);
-  else zero_kernel<<<grid, kThreads, 0, stream>>>(static_cast<float*>(p), n);
+  const dim3 grid(static_cast<unsigned>((n + 255) / 256));
+  if (dtype == kRowBf16) zero_kernel<<<grid, 256, 0, stream>>>(static_cast<uint16_t*>(p), n);
+  else zero_kernel<<<grid, 256, 0, stream>>>(static_cast<float*>(p), n);
   return hipGetLastError();
 }
 
