@@ -150,7 +150,6 @@ int w4_matvec_multi(int64_t T, int64_t d_in, int32_t n_proj, const int64_t* d_ou
     if (!aligned16(codes[g]) || !aligned16(scales[g]) || !aligned16(z) || !aligned16(y[g])) return LN_EALIGN;
     tiles += (d_out[g] + 15) / 16;
     if (tiles > (int64_t(1) << 27)) return LN_ESHAPE;
-    tab.row_end[g] = static_cast<int>(tiles);
     tab.N[g] = static_cast<int>(d_out[g]);
     tab.codes[g] = codes[g];
     tab.scales[g] = scales[g];

@@ -28,10 +28,11 @@ hipError_t launch_w4_dequantize(const uint8_t* codes, const uint16_t* scales, co
                                 int64_t K, int group, bool out_bf16, void* out, hipStream_t stream);
 
 constexpr int kW4MaxProj = 8;
-// Weights of one launch; row_end[g] = 16-row tiles of weights 0 .. g.
+// Weights of one launch; group_end[g] (set by the launcher) = workgroups along the rows
+// of weights 0 .. g.
 struct W4Table {
   int n;
-  int row_end[kW4MaxProj];
+  int group_end[kW4MaxProj];
   int N[kW4MaxProj];
   const uint8_t* codes[kW4MaxProj];
   const uint16_t* scales[kW4MaxProj];
