@@ -107,6 +107,12 @@ struct Rows<kRowI8> {
   }
 };
 
+// Nothing is moved across: the counted waits rely on the order that loads are issued in.
+__device__ __forceinline__ void keep_order() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+}
+
 // v of lane 16 j + (lane & 15) in every lane, for a v that differs between the four
 // lane rows (GP = 4) or the two lane halves (GP = 2): j = 0 .. GP - 1.
 template <int GP>
@@ -280,21 +286,255 @@ __global__ __launch_bounds__(W * 64) void w4_matvec_kernel(int64_t T, int K, con
   }
 }
 
-// One launch of the kernel <XT, TB, R, W, D> for the table's group size and zero points.
-template <int XT, int TB, int R, int W, int D>
+// More rows of x: the x operands of a chunk, 16 TB rows, outweigh its codes, so the
+// waves of a workgroup share them through LDS. RW x KW waves: each row wave owns R
+// tiles, the KW waves of a row wave take the chunks of a step (KW chunks) in turn. x of
+// a step is copied straight to LDS (a ring of NS steps, one barrier a step; 16-byte
+// pieces XOR-swizzled by row so that operand reads spread over the banks), codes run NS
+// steps ahead in registers. Every load is issued whether its step exists or not (the
+// last step's again past the end), so the counts that the waits rely on are constant.
+// The ring's slots are arrays of their own: with one array the compiler lets operand
+// reads of one slot wait for the copies in flight to the others.
+template <int XT, int TB, int R, int RW, int KW, int NS, int G, bool ZERO>
+__global__ __launch_bounds__(RW * KW * 64) void w4_matvec_shared_kernel(int64_t T, int K, const uint8_t* __restrict__ x,
+                                                                        const float* __restrict__ x_scale,
+                                                                        const W4Table tab, int t_blocks, bool y_bf16) {
+  using X = Rows<XT>;
+  using Op = typename X::Op;
+  using Acc = typename X::Acc;
+  constexpr int GP = 128 / G, kWaves = RW * KW;
+  constexpr int kRowBytes = 128 * X::kBytes, kChunk = 16 * TB * kRowBytes, kStage = KW * kChunk;
+  constexpr int kCopies = kStage / 1024, kPer = (kCopies + kWaves - 1) / kWaves;  // 1 KB copies, and a wave's share
+  constexpr int kPieces = kRowBytes / 16, kCopyRows = 64 / kPieces;
+  static_assert(NS == 3, "one array a slot");
+  __shared__ __align__(1024) unsigned char slot0[kStage];
+  __shared__ __align__(1024) unsigned char slot1[kStage];
+  __shared__ __align__(1024) unsigned char slot2[kStage];
+  __shared__ float sums[KW > 1 ? KW - 1 : 1][RW][R * TB * 4][64];
+  const int lane = threadIdx.x & 63, l16 = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), rw = wave % RW, kw = wave / RW;
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x % t_blocks) * (16 * TB);
+  int group = blockIdx.x / t_blocks, p = 0;
+  while (group >= tab.group_end[p]) ++p;
+  if (p > 0) group -= tab.group_end[p - 1];
+  const int N = tab.N[p], nt = (N + 15) / 16, kt = (K + 127) / 128, kg = K / G;
+  const int steps = (kt + KW - 1) / KW;
+  const int tile0 = (group * RW + rw) * R;
+  __amdgpu_buffer_rsrc_t code_rs[R], scale_rs[R], zero_rs[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int64_t tile = min(tile0 + r, nt - 1);
+    code_rs[r] = make_rsrc(tab.codes[p] + tile * kt * 1024, kt * 1024);
+    scale_rs[r] = make_rsrc(tab.scales[p] + tile * kg * 16, kg * 32);
+    if constexpr (ZERO) zero_rs[r] = make_rsrc(tab.zeros[p] + tile * kg * 16, kg * 16);
+  }
+  const int rows = static_cast<int>(min(T - t0, static_cast<int64_t>(16 * TB)));
+  const auto x_rs = make_rsrc(x + t0 * K * X::kBytes, static_cast<uint32_t>(rows) * K * X::kBytes);
+  const uint32_t group_at = (GP == 1 ? 0 : GP == 2 ? g >> 1 : g) * 16 + l16;
+  const uint32_t group_at_half = (GP == 4 ? g & 1 : 0) * 16 + l16;
+  // Copy c of a stage fills its bytes 1024 c ..: rows kCopyRows c .. of a chunk, lane L the
+  // physical piece L % kPieces of row L / kPieces, which holds the logical piece
+  // (physical ^ row) (mod kPieces).
+  int copy_c[kPer];
+  uint32_t copy_at[kPer];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    copy_c[i] = (wave + kWaves * i) % kCopies;
+    const int row = copy_c[i] * kCopyRows % (16 * TB) + lane / kPieces;
+    const int piece = (lane ^ row) & (kPieces - 1);
+    copy_at[i] = static_cast<uint32_t>(min(row, rows - 1)) * K * X::kBytes + 16 * piece;
+  }
+  const bool has_half = GP > 1 && (K & 64) != 0;
+  auto load_x = [&](int i, unsigned char* stage) {
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const int at = min(i * KW + copy_c[j] * 1024 / kChunk, kt - 1);
+      uint32_t off = copy_at[j];
+      // (in place of the half that a last chunk lacks, the first one; the step clears it)
+      if (has_half && at == kt - 1) off -= ((lane ^ (copy_c[j] * kCopyRows + lane / kPieces)) & (kPieces / 2)) * 16;
+      buf_load16_lds(x_rs, stage + copy_c[j] * 1024, off, at * kRowBytes);
+    }
+  };
+  struct Chunk {
+    uint4 codes[R];
+    uint32_t scale[R], zero[R];
+  };
+  Chunk ring[NS];
+  auto load_w = [&](int i, Chunk& c) {
+    const int at = min(i * KW + kw, kt - 1);
+    const uint32_t ga = has_half && at == kt - 1 ? group_at_half : group_at;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      c.codes[r] = buf_load16(code_rs[r], lane * 16, at * 1024);
+      c.scale[r] = buf_load2(scale_rs[r], ga * 2, at * (GP * 32));
+      if constexpr (ZERO) c.zero[r] = buf_load1(zero_rs[r], ga, at * (GP * 16));
+    }
+  };
+  float tot[R][TB][4];
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int b = 0; b < TB; ++b)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) tot[r][b][j] = 0.f;
+  const typename X::Wide minus = X::minus(!ZERO);
+  // operand q of row block b: 8 elements at 32 q + 8 g of row 16 b + l16
+  auto x_op = [&](const unsigned char* chunk, int b, int q) {
+    const int row = 16 * b + l16, byte = (32 * q + 8 * g) * X::kBytes;
+    const int piece = ((byte >> 4) ^ row) & (kPieces - 1);
+    return *reinterpret_cast<const Op*>(chunk + row * kRowBytes + 16 * piece + (byte & 15));
+  };
+  auto step = [&](int i, const Chunk& c, const unsigned char* stage) {
+    const int at = i * KW + kw;
+    if (at >= kt) return;  // the last step may lack a chunk
+    const bool half = has_half && at == kt - 1;
+    const unsigned char* const chunk = stage + kw * kChunk;
+    float s[R][GP], z[R][GP];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      uint32_t v[GP];
+      spread<GP>(c.scale[r] | (ZERO ? c.zero[r] << 16 : 0u), v);
+#pragma unroll
+      for (int j = 0; j < GP; ++j) {
+        s[r][j] = __uint_as_float(v[j] << 16);
+        if constexpr (ZERO) z[r][j] = static_cast<float>(v[j] >> 16);
+      }
+    }
+    Acc acc[R][TB], xs[TB];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const bool first = q * 32 % G == 0;
+      typename X::Wide xq[TB];
+#pragma unroll
+      for (int b = 0; b < TB; ++b) {
+        Op o = x_op(chunk, b, q);
+        if (q >= 2 && half) o = Op{};
+        xq[b] = X::widen(o);
+        xs[b] = X::mma(xq[b], minus, first ? Acc{} : xs[b]);
+      }
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const uint32_t words[4] = {c.codes[r].x, c.codes[r].y, c.codes[r].z, c.codes[r].w};
+        const typename X::Wide w = X::codes(words[q]);
+#pragma unroll
+        for (int b = 0; b < TB; ++b) acc[r][b] = X::mma(xq[b], w, first ? Acc{} : acc[r][b]);
+      }
+      if ((q + 1) * 32 % G == 0) {
+        const int j = q * 32 / G;
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+          for (int b = 0; b < TB; ++b)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              float u;
+              if constexpr (ZERO)
+                u = static_cast<float>(acc[r][b][e]) + z[r][j] * static_cast<float>(xs[b][e]);
+              else
+                u = static_cast<float>(acc[r][b][e] + xs[b][e]);
+              tot[r][b][e] += s[r][j] * u;
+            }
+      }
+    }
+  };
+  // Order of a wave's loads: x of steps 0 .. NS - 2, codes of steps 0 .. NS - 1; then in
+  // step i x of step i + NS - 1 and codes of step i + NS. Loads retire in order, so the x
+  // of step i has landed when at most as many loads are outstanding as were issued after
+  // it: x of NS - 2 steps and codes of NS - 1 (more at the start).
+  constexpr int kCodes = R * (ZERO ? 3 : 2);
+  constexpr int kWait = (NS - 2) * kPer + (NS - 1) * kCodes;
+  static_assert(kWait < 64, "load counter");
+  load_x(0, slot0);
+  load_x(1, slot1);
+  keep_order();
+#pragma unroll
+  for (int d = 0; d < NS; ++d) {
+    load_w(d, ring[d]);
+    keep_order();
+  }
+  auto turn = [&](int i, Chunk& c, const unsigned char* mine, unsigned char* next) {
+    wait_vmem_upto<kWait>();
+    __syncthreads();  // x of this step is whole, and the step that used `next` is over
+    load_x(i + NS - 1, next);
+    keep_order();
+    step(i, c, mine);
+    keep_order();
+    load_w(i + NS, c);
+    keep_order();
+  };
+  for (int i = 0; i < steps; i += NS) {
+    turn(i, ring[0], slot0, slot2);
+    if (i + 1 < steps) turn(i + 1, ring[1], slot1, slot0);
+    if (i + 2 < steps) turn(i + 2, ring[2], slot2, slot1);
+  }
+  wait_vmem();  // run-ahead copies land before the workgroup gives its LDS back
+  if constexpr (KW > 1) {
+    if (kw > 0) {
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int b = 0; b < TB; ++b)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sums[kw - 1][rw][(r * TB + b) * 4 + e][lane] = tot[r][b][e];
+    }
+    __syncthreads();
+    if (kw > 0) return;
+  }
+  float factor[TB][4];
+#pragma unroll
+  for (int b = 0; b < TB; ++b)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int64_t t = min(t0 + 16 * b + 4 * g + e, T - 1);
+      factor[b][e] = x_scale != nullptr ? x_scale[t] : 1.f;
+    }
+  auto finish = [&](auto* y) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int n = (tile0 + r) * 16 + l16;
+#pragma unroll
+      for (int b = 0; b < TB; ++b)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int64_t t = t0 + 16 * b + 4 * g + e;
+          float v = tot[r][b][e];
+          if constexpr (KW > 1)
+#pragma unroll
+            for (int k = 0; k < KW - 1; ++k) v += sums[k][rw][(r * TB + b) * 4 + e][lane];
+          v *= factor[b][e];
+          if (t < T && n < N) {
+            if constexpr (sizeof(*y) == 2) y[t * N + n] = to_bf16(v);
+            else y[t * N + n] = v;
+          }
+        }
+    }
+  };
+  if (y_bf16) finish(static_cast<uint16_t*>(tab.y[p]));
+  else finish(static_cast<float*>(tab.y[p]));
+}
+
+// One launch for the table's group size and zero points: the kernel with K-split waves
+// (SHARED = 0: <XT, TB, R, W, D>) or the one with x in LDS (<XT, TB, R, RW, KW, NS = SHARED>).
+template <int XT, int TB, int R, int A, int B, int SHARED = 0>
 hipError_t run(int64_t T, int K, int group, const void* x, const float* x_scale, W4Table tab, bool y_bf16,
                hipStream_t stream) {
+  constexpr int kTiles = SHARED > 0 ? R * A : R;
   int groups = 0;
   for (int p = 0; p < tab.n; ++p) {
-    groups += ((tab.N[p] + 15) / 16 + R - 1) / R;
+    groups += ((tab.N[p] + 15) / 16 + kTiles - 1) / kTiles;
     tab.group_end[p] = groups;
   }
   const int t_blocks = static_cast<int>((T + 16 * TB - 1) / (16 * TB));
   const dim3 grid(static_cast<unsigned>(groups) * static_cast<unsigned>(t_blocks));
   const auto xb = static_cast<const uint8_t*>(x);
   auto go = [&](auto g, auto zero) {
-    w4_matvec_kernel<XT, TB, R, W, D, decltype(g)::value, decltype(zero)::value>
-        <<<grid, W * 64, 0, stream>>>(T, K, xb, x_scale, tab, t_blocks, y_bf16);
+    constexpr int kG = decltype(g)::value;
+    constexpr bool kZero = decltype(zero)::value;
+    if constexpr (SHARED > 0)
+      w4_matvec_shared_kernel<XT, TB, R, A, B, SHARED, kG, kZero>
+          <<<grid, A * B * 64, 0, stream>>>(T, K, xb, x_scale, tab, t_blocks, y_bf16);
+    else
+      w4_matvec_kernel<XT, TB, R, A, B, kG, kZero><<<grid, A * 64, 0, stream>>>(T, K, xb, x_scale, tab, t_blocks, y_bf16);
   };
   auto with = [&](auto zero) {
     if (group == 32) go(std::integral_constant<int, 32>{}, zero);
@@ -316,8 +556,8 @@ hipError_t pick(int64_t T, int K, int group, const void* x, const float* x_scale
     if (tiles <= 768) return run<XT, 1, 2, 8, 2>(T, K, group, x, x_scale, tab, y_bf16, stream);
     return run<XT, 1, 4, 8, 1>(T, K, group, x, x_scale, tab, y_bf16, stream);
   }
-  if (T <= 32) return run<XT, 2, 4, 8, 1>(T, K, group, x, x_scale, tab, y_bf16, stream);
-  return run<XT, 4, 4, 4, 1>(T, K, group, x, x_scale, tab, y_bf16, stream);
+  if (T <= 32) return run<XT, 2, 2, 4, 2, 3>(T, K, group, x, x_scale, tab, y_bf16, stream);
+  return run<XT, 4, 2, 4, 2, 3>(T, K, group, x, x_scale, tab, y_bf16, stream);
 }
 
 }  // namespace

@@ -16,6 +16,7 @@ graph. Gradients are functions of their own, not autograd nodes.
 from __future__ import annotations
 
 import ctypes
+from array import array
 
 import torch
 
@@ -43,50 +44,53 @@ NORM_W4_SYMBOLS = tuple(_NORM_W4_SIGS)
 _PLAIN = {torch.float32: LN_F32, torch.bfloat16: LN_BF16}
 _EIGHT = {torch.float8_e4m3fn: LN_E4M3, torch.int8: LN_I8}
 _X = {torch.bfloat16: LN_BF16, **_EIGHT}
+_GROUPS = (32, 64, 128)
 
 
 def _code(table, dtype, name):
-    try:
-        return table[dtype]
-    except KeyError:
-        raise ValueError(f"{name} must have one of the dtypes {[str(t) for t in table]}, got {dtype}") from None
+    code = table.get(dtype)
+    if code is None:
+        raise ValueError(f"{name} must have one of the dtypes {[str(t) for t in table]}, got {dtype}")
+    return code
 
+
+# One decoded token is a few microseconds of GPU time, so the checks below are written to
+# cost little where they pass: one conjunction, and the reason worked out only on failure.
 
 def _lead(t, name, ndim):
     """The device index of the tensor that decides where a call runs."""
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.dim() == ndim and t.is_contiguous():
+        return t.get_device()
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a GPU tensor")
     if t.dim() != ndim:
         raise ValueError(f"{name} must be {ndim}-D")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.get_device()
+    raise ValueError(f"{name} must be contiguous")
 
 
-def _like(t, name, dev, dtype, shape):
-    """The address of an operand on device `dev`, of a dtype and shape; None stays None."""
-    if t is None:
-        return None
+def _at(t, name, dev, dtype, shape):
+    """The address of an operand on device `dev`, of a dtype and shape."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == dev and \
+            t.is_contiguous():
+        return t.data_ptr()
     if not isinstance(t, torch.Tensor) or not t.is_cuda or t.get_device() != dev:
         raise ValueError(f"{name} must be a tensor on GPU {dev}")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise ValueError(f"{name} must have dtype {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _call(name, dev, *args):
     """The C entry point on the current stream of device `dev` (made the current device
     for the launch, where it is not)."""
     fn = getattr(library(), name)
-    if torch.cuda.current_device() == dev:
-        st = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    if torch._C._cuda_getDevice() == dev:
+        st = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
     else:
         with torch.cuda.device(dev):
-            st = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+            st = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
     if st != LN_OK:
         raise LoraNF4Error(name, st)
 
@@ -95,11 +99,8 @@ def _norm_args(x, weight, residual):
     dev = _lead(x, "x", 2)
     kind = _code(_PLAIN, x.dtype, "x")
     T, d = x.shape
-    w = _like(weight, "weight", dev, x.dtype, (d,))
-    if w is None:
-        raise ValueError("weight must be given")
-    r = _like(residual, "residual", dev, x.dtype, x.shape)
-    return dev, kind, T, d, w, r
+    w = _at(weight, "weight", dev, x.dtype, (d,))
+    return dev, kind, T, d, w, None if residual is None else _at(residual, "residual", dev, x.dtype, (T, d))
 
 
 def rmsnorm_fwd(x, weight, eps: float = 1e-5, residual=None, save_rstd: bool = True):
@@ -109,7 +110,7 @@ def rmsnorm_fwd(x, weight, eps: float = 1e-5, residual=None, save_rstd: bool = T
     dev, kind, T, d, w, r = _norm_args(x, weight, residual)
     y = torch.empty_like(x)
     h = x if residual is None else torch.empty_like(x)
-    rstd = torch.empty(T, dtype=torch.float32, device=x.device) if save_rstd else None
+    rstd = x.new_empty(T, dtype=torch.float32) if save_rstd else None
     _call("rmsnorm_fwd", dev, T, d, kind, eps, x.data_ptr(), r, w, None if r is None else h.data_ptr(),
           y.data_ptr(), None if rstd is None else rstd.data_ptr())
     return y, h, rstd
@@ -121,7 +122,7 @@ def rmsnorm_fwd_quant(x, weight, eps: float = 1e-5, residual=None, qdtype=torch.
     dev, kind, T, d, w, r = _norm_args(x, weight, residual)
     fmt = _code(_EIGHT, qdtype, "qdtype")
     q = torch.empty_like(x, dtype=qdtype)
-    scale = torch.empty(T, dtype=torch.float32, device=x.device)
+    scale = x.new_empty(T, dtype=torch.float32)
     h = x if residual is None else torch.empty_like(x)
     _call("rmsnorm_fwd_quant", dev, T, d, kind, eps, x.data_ptr(), r, w, None if r is None else h.data_ptr(), fmt,
           q.data_ptr(), scale.data_ptr())
@@ -138,12 +139,10 @@ def rmsnorm_bwd(dy, h, weight, rstd, dh=None, need_dw: bool = True, workspace: t
     dev = _lead(h, "h", 2)
     kind = _code(_PLAIN, h.dtype, "h")
     T, d = h.shape
-    w = _like(weight, "weight", dev, h.dtype, (d,))
-    g = _like(dy, "dy", dev, h.dtype, h.shape)
-    r = _like(rstd, "rstd", dev, torch.float32, (T,))
-    if w is None or g is None or r is None:
-        raise ValueError("dy, weight and rstd must be given")
-    e = _like(dh, "dh", dev, h.dtype, h.shape)
+    w = _at(weight, "weight", dev, h.dtype, (d,))
+    g = _at(dy, "dy", dev, h.dtype, (T, d))
+    r = _at(rstd, "rstd", dev, torch.float32, (T,))
+    e = None if dh is None else _at(dh, "dh", dev, h.dtype, (T, d))
     dx = torch.empty_like(h)
     dw = torch.empty_like(weight) if need_dw else None
     ws = _workspace(rmsnorm_bwd_workspace_bytes(T, d), workspace, h.device) if need_dw else None
@@ -160,12 +159,12 @@ def w4_quantize(w, group: int = 128, zero_points: bool = False):
     dev = _lead(w, "w", 2)
     kind = _code(_PLAIN, w.dtype, "w")
     N, K = w.shape
-    if group not in (32, 64, 128):
+    if group not in _GROUPS:
         raise ValueError(f"group must be 32, 64 or 128, got {group}")
     nt, kt, kg = (N + 15) // 16, (K + 127) // 128, K // group
-    codes = torch.empty((nt, kt, 1024), dtype=torch.uint8, device=w.device)
-    scales = torch.empty((nt, kg, 16), dtype=torch.bfloat16, device=w.device)
-    zeros = torch.empty((nt, kg, 16), dtype=torch.uint8, device=w.device) if zero_points else None
+    codes = w.new_empty((nt, kt, 1024), dtype=torch.uint8)
+    scales = w.new_empty((nt, kg, 16), dtype=torch.bfloat16)
+    zeros = w.new_empty((nt, kg, 16), dtype=torch.uint8) if zero_points else None
     _call("w4_quantize", dev, w.data_ptr(), kind, N, K, group, codes.data_ptr(), scales.data_ptr(),
           None if zeros is None else zeros.data_ptr())
     return codes, scales, zeros
@@ -173,22 +172,19 @@ def w4_quantize(w, group: int = 128, zero_points: bool = False):
 
 def _packed(codes, scales, zeros, d_in, d_out, dev, tag=""):
     """(d_out, group, addresses) of a packed weight whose rows are d_in wide."""
-    if not isinstance(scales, torch.Tensor) or scales.dim() != 3 or not scales.shape[1]:
+    if not isinstance(scales, torch.Tensor) or scales.dim() != 3:
         raise ValueError(f"scales{tag} must be [ceil(d_out / 16), d_in / group, 16]")
-    nt, kg = scales.shape[:2]
-    group = d_in // kg
-    if kg * group != d_in or group not in (32, 64, 128):
+    nt, kg, _ = shape = scales.shape
+    group = d_in // kg if kg else 0
+    if kg * group != d_in or group not in _GROUPS:
         raise ValueError(f"scales{tag} hold {kg} groups of a row: d_in {d_in} makes no group of 32, 64 or 128")
     if d_out is None:
         d_out = 16 * nt
-    if not 16 * (nt - 1) < d_out <= 16 * nt:
+    elif not 16 * (nt - 1) < d_out <= 16 * nt:
         raise ValueError(f"d_out{tag} {d_out} does not fit scales{tag} of {nt} tiles of 16 rows")
-    c = _like(codes, f"codes{tag}", dev, torch.uint8, (nt, (d_in + 127) // 128, 1024))
-    s = _like(scales, f"scales{tag}", dev, torch.bfloat16, (nt, kg, 16))
-    z = _like(zeros, f"zeros{tag}", dev, torch.uint8, (nt, kg, 16))
-    if c is None:
-        raise ValueError(f"codes{tag} must be given")
-    return d_out, group, c, s, z
+    c = _at(codes, f"codes{tag}", dev, torch.uint8, (nt, (d_in + 127) // 128, 1024))
+    s = _at(scales, f"scales{tag}", dev, torch.bfloat16, (nt, kg, 16))
+    return d_out, group, c, s, 0 if zeros is None else _at(zeros, f"zeros{tag}", dev, torch.uint8, shape)
 
 
 def w4_dequantize(codes, scales, zeros=None, *, d_out: int | None = None, d_in: int | None = None,
@@ -199,15 +195,15 @@ def w4_dequantize(codes, scales, zeros=None, *, d_out: int | None = None, d_in: 
     kind = _code(_PLAIN, dtype, "dtype")
     K = codes.shape[1] * 128 if d_in is None else d_in
     N, group, c, s, z = _packed(codes, scales, zeros, K, d_out, dev)
-    out = torch.empty((N, K), dtype=dtype, device=codes.device)
+    out = codes.new_empty((N, K), dtype=dtype)
     _call("w4_dequantize", dev, c, s, z, N, K, group, kind, out.data_ptr())
     return out
 
 
 def _x_args(x, x_scale, dtype):
     dev = _lead(x, "x", 2)
-    return dev, _code(_X, x.dtype, "x"), _like(x_scale, "x_scale", dev, torch.float32, (x.shape[0],)), \
-        _code(_PLAIN, dtype, "dtype")
+    return dev, _code(_X, x.dtype, "x"), None if x_scale is None else \
+        _at(x_scale, "x_scale", dev, torch.float32, (x.shape[0],)), _code(_PLAIN, dtype, "dtype")
 
 
 def w4_matvec(x, codes, scales, zeros=None, *, d_out: int | None = None, x_scale=None, dtype=torch.bfloat16,
@@ -218,8 +214,11 @@ def w4_matvec(x, codes, scales, zeros=None, *, d_out: int | None = None, x_scale
     T, K = x.shape
     N, group, c, s, z = _packed(codes, scales, zeros, K, d_out, dev)
     if out is None:
-        out = torch.empty((T, N), dtype=dtype, device=x.device)
-    _call("w4_matvec", dev, T, K, N, group, xt, x.data_ptr(), xs, c, s, z, yt, _like(out, "out", dev, dtype, (T, N)))
+        out = x.new_empty((T, N), dtype=dtype)
+        y = out.data_ptr()
+    else:
+        y = _at(out, "out", dev, dtype, (T, N))
+    _call("w4_matvec", dev, T, K, N, group, xt, x.data_ptr(), xs, c, s, z, yt, y)
     return out
 
 
@@ -232,15 +231,16 @@ def w4_matvec_multi(x, codes, scales, zeros=None, *, d_out=None, x_scale=None, d
     if not 1 <= n <= LN_MAX_PROJ or len(scales) != n or (zeros is not None and len(zeros) != n) or \
             (d_out is not None and len(d_out) != n):
         raise ValueError(f"codes, scales (zeros, d_out) must be lists of the same length, 1 to {LN_MAX_PROJ}")
-    ws = [_packed(codes[g], scales[g], None if zeros is None else zeros[g], K, None if d_out is None else d_out[g],
-                  dev, f"[{g}]") for g in range(n)]
-    if any(w[1] != ws[0][1] for w in ws):
+    N, groups, c, s, z = zip(*(_packed(codes[g], scales[g], None if zeros is None else zeros[g], K,
+                                       None if d_out is None else d_out[g], dev, f"[{g}]") for g in range(n)))
+    if len(set(groups)) > 1:
         raise ValueError("all weights must share the group size")
-    if any((w[4] is None) != (ws[0][4] is None) for w in ws):
+    if not all(z) and any(z):
         raise ValueError("zeros must be given for every weight or for none")
-    ys = [torch.empty((T, w[0]), dtype=dtype, device=x.device) for w in ws]
-    arr = _p * n
-    _call("w4_matvec_multi", dev, T, K, n, (_i64 * n)(*(w[0] for w in ws)), ws[0][1], xt, x.data_ptr(), xs,
-          arr(*(w[2] for w in ws)), arr(*(w[3] for w in ws)),
-          None if ws[0][4] is None else arr(*(w[4] for w in ws)), yt, arr(*(y.data_ptr() for y in ys)))
+    ys = [x.new_empty((T, w), dtype=dtype) for w in N]
+    # the five arrays of the C call side by side (read during the call only)
+    table = array("q", (*N, *c, *s, *z, *(y.data_ptr() for y in ys)))
+    at, _ = table.buffer_info()
+    _call("w4_matvec_multi", dev, T, K, n, at, groups[0], xt, x.data_ptr(), xs, at + 8 * n, at + 16 * n,
+          at + 24 * n if z[0] else None, yt, at + 32 * n)
     return ys
