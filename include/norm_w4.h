@@ -116,25 +116,36 @@ int w4_dequantize(const uint8_t* codes, const uint16_t* scales, const uint8_t* z
  *   x         [T, d_in] of x_dtype: LN_BF16, LN_E4M3 or LN_I8
  *   x_scale   float32 [T], one factor a row (rmsnorm_fwd_quant's q_scale), or NULL (1)
  *   y         [T, d_out] of y_dtype: LN_BF16 or LN_F32
- * Any T >= 0; made for up to 64 rows, where reading the packed weight bounds it. More
+ *   workspace w4_matvec_workspace_bytes(T, d_in, d_out) bytes (0 unless d_in is split
+ *             across workgroups, where the float32 sums of the splits meet in it, added in
+ *             a fixed order); may be NULL when that is 0
+ * 0 <= T <= 2^21; made for up to 64 rows, where reading the packed weight bounds it. More
  * rows run as blocks of 64, each reading the weight again.
  */
 int w4_matvec(int64_t T, int64_t d_in, int64_t d_out, int32_t group, int x_dtype, const void* x,
               const float* x_scale, const uint8_t* codes, const uint16_t* scales, const uint8_t* zeros,
-              int y_dtype, void* y, void* stream);
+              int y_dtype, void* y, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes w4_matvec needs (0 if the sizes are invalid, T = 0, or none is needed). */
+size_t w4_matvec_workspace_bytes(int64_t T, int64_t d_in, int64_t d_out);
 
 /*
  * w4_matvec_multi — w4_matvec of n_proj weights that read the same x (q/k/v, gate/up)
- * in one launch; the values are those of n_proj calls.
+ * in one launch (and one more where d_in is split).
  *   d_out, codes, scales, zeros, y   HOST arrays [n_proj] (1 .. LN_MAX_PROJ), read
  *             during the call only; zeros NULL: no weight has zero points, otherwise
  *             every entry is given
- * All weights share d_in and group.
+ *   workspace as for w4_matvec, sized by w4_matvec_multi_workspace_bytes
+ * All weights share d_in and group. (The values are those of single calls up to the
+ * order of float32 additions, where the two split d_in differently.)
  */
 int w4_matvec_multi(int64_t T, int64_t d_in, int32_t n_proj, const int64_t* d_out, int32_t group,
                     int x_dtype, const void* x, const float* x_scale, const uint8_t* const* codes,
                     const uint16_t* const* scales, const uint8_t* const* zeros, int y_dtype,
-                    void* const* y, void* stream);
+                    void* const* y, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes w4_matvec_multi needs (0 if the sizes are invalid, T = 0, or none is needed). */
+size_t w4_matvec_multi_workspace_bytes(int64_t T, int64_t d_in, int32_t n_proj, const int64_t* d_out);
 
 #ifdef __cplusplus
 }

@@ -53,6 +53,7 @@ int check_w4(int64_t N, int64_t K, int32_t group) {
   if ((N + 15) / 16 * ((K + 127) / 128) > (int64_t(1) << 30)) return LN_ESHAPE;
   return LN_OK;
 }
+constexpr int64_t kMaxW4Rows = int64_t(1) << 21;  // rows of x (the grid stays below 2^31 workgroups)
 size_t w4_code_bytes(int64_t N, int64_t K) { return static_cast<size_t>((N + 15) / 16 * ((K + 127) / 128)) * 1024; }
 size_t w4_groups(int64_t N, int64_t K, int32_t group) { return static_cast<size_t>((N + 15) / 16 * (K / group)) * 16; }
 
@@ -127,16 +128,31 @@ int w4_dequantize(const uint8_t* codes, const uint16_t* scales, const uint8_t* z
                                          static_cast<hipStream_t>(stream)));
 }
 
+size_t w4_matvec_multi_workspace_bytes(int64_t T, int64_t d_in, int32_t n_proj, const int64_t* d_out) {
+  if (T < 1 || T > kMaxW4Rows || n_proj < 1 || n_proj > LN_MAX_PROJ || d_out == nullptr) return 0;
+  int N[LN_MAX_PROJ];
+  for (int g = 0; g < n_proj; ++g) {
+    if (check_w4(d_out[g], d_in, 32) != LN_OK) return 0;
+    N[g] = static_cast<int>(d_out[g]);
+  }
+  return w4_matvec_bytes(T, d_in, n_proj, N);
+}
+
+size_t w4_matvec_workspace_bytes(int64_t T, int64_t d_in, int64_t d_out) {
+  return w4_matvec_multi_workspace_bytes(T, d_in, 1, &d_out);
+}
+
 int w4_matvec_multi(int64_t T, int64_t d_in, int32_t n_proj, const int64_t* d_out, int32_t group, int x_dtype,
                     const void* x, const float* x_scale, const uint8_t* const* codes, const uint16_t* const* scales,
-                    const uint8_t* const* zeros, int y_dtype, void* const* y, void* stream) {
+                    const uint8_t* const* zeros, int y_dtype, void* const* y, void* workspace,
+                    size_t workspace_bytes, void* stream) {
   if (n_proj < 1 || n_proj > LN_MAX_PROJ || T < 0) return LN_EINVAL;
   if (d_out == nullptr || codes == nullptr || scales == nullptr || y == nullptr) return LN_EINVAL;
   if (T != 0 && x == nullptr) return LN_EINVAL;
   if ((x_dtype != LN_BF16 && x_dtype != LN_E4M3 && x_dtype != LN_I8) || !plain_type(y_dtype)) return LN_EINVAL;
   static_assert(LN_MAX_PROJ <= kW4MaxProj, "table size");
   W4Table tab{};
-  Span outs[LN_MAX_PROJ], ins[3 * LN_MAX_PROJ + 2];
+  Span outs[LN_MAX_PROJ + 1], ins[3 * LN_MAX_PROJ + 2];
   int n_in = 0;
   int64_t tiles = 0;
   const size_t t = static_cast<size_t>(T);
@@ -161,20 +177,25 @@ int w4_matvec_multi(int64_t T, int64_t d_in, int32_t n_proj, const int64_t* d_ou
     ins[n_in++] = {scales[g], gs * 2};
     ins[n_in++] = {z, gs};
   }
-  if (T > (int64_t(1) << 21)) return LN_ESHAPE;
+  if (T > kMaxW4Rows) return LN_ESHAPE;
   if (T == 0) return LN_OK;
   if (!aligned16(x) || !aligned16(x_scale)) return LN_EALIGN;
+  const size_t need = w4_matvec_bytes(T, d_in, n_proj, tab.N);
+  if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return LN_EWORKSPACE;
+  if (need > 0 && (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return LN_EALIGN;
+  outs[n_proj] = {need > 0 ? workspace : nullptr, need};
   ins[n_in++] = {x, t * static_cast<size_t>(d_in) * type_bytes(x_dtype)};
   ins[n_in++] = {x_scale, t * 4};
-  if (any_alias(outs, n_proj, ins, n_in)) return LN_EALIAS;
+  if (any_alias(outs, n_proj + 1, ins, n_in)) return LN_EALIAS;
   return hip_status(launch_w4_matvec(T, static_cast<int>(d_in), group, x_dtype, x, x_scale, tab, y_dtype == LN_BF16,
-                                     static_cast<hipStream_t>(stream)));
+                                     workspace, static_cast<hipStream_t>(stream)));
 }
 
 int w4_matvec(int64_t T, int64_t d_in, int64_t d_out, int32_t group, int x_dtype, const void* x, const float* x_scale,
-              const uint8_t* codes, const uint16_t* scales, const uint8_t* zeros, int y_dtype, void* y, void* stream) {
+              const uint8_t* codes, const uint16_t* scales, const uint8_t* zeros, int y_dtype, void* y,
+              void* workspace, size_t workspace_bytes, void* stream) {
   return w4_matvec_multi(T, d_in, 1, &d_out, group, x_dtype, x, x_scale, &codes, &scales,
-                         zeros == nullptr ? nullptr : &zeros, y_dtype, &y, stream);
+                         zeros == nullptr ? nullptr : &zeros, y_dtype, &y, workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"

@@ -39,7 +39,9 @@ struct W4Table {
   const uint8_t* zeros[kW4MaxProj];
   void* y[kW4MaxProj];
 };
+// Bytes of float32 partial sums, where d_in is split across workgroups (else 0).
+size_t w4_matvec_bytes(int64_t T, int64_t K, int n, const int* N);
 hipError_t launch_w4_matvec(int64_t T, int K, int group, int x_type, const void* x, const float* x_scale,
-                            const W4Table& tab, bool y_bf16, hipStream_t stream);
+                            const W4Table& tab, bool y_bf16, void* workspace, hipStream_t stream);
 
 }  // namespace lnf4

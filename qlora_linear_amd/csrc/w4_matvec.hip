@@ -185,7 +185,7 @@ __global__ __launch_bounds__(W * 64) void w4_matvec_kernel(int64_t T, int K, con
       c.scale[r] = buf_load2(scale_rs[r], ga * 2, at * (GP * 32));
       if constexpr (ZERO) c.zero[r] = buf_load1(zero_rs[r], ga, at * (GP * 16));
     }
-    // (in place of a half that does not exist the first one is read; the step clears it)
+    // (in place of a half that does not exist the first one is read; its scales become 0)
     const uint32_t x0 = at * 128 * X::kBytes, x1 = x0 + (half ? 0 : 64 * X::kBytes);
 #pragma unroll
     for (int b = 0; b < TB; ++b)
@@ -202,15 +202,12 @@ __global__ __launch_bounds__(W * 64) void w4_matvec_kernel(int64_t T, int K, con
       for (int j = 0; j < 4; ++j) tot[r][b][j] = 0.f;
   const typename X::Wide minus = X::minus(!ZERO);
   auto step = [&](int i, Chunk& c) {
-    if (GP > 1 && (wave + W * i) * 128 + 64 == K) {
-#pragma unroll
-      for (int b = 0; b < TB; ++b) c.x[b][2] = c.x[b][3] = Op{};
-    }
+    const bool absent = GP > 1 && (wave + W * i) * 128 + 64 == K && g >= 2;  // the lane's group
     float s[R][GP], z[R][GP];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       uint32_t v[GP];
-      spread<GP>(c.scale[r] | (ZERO ? c.zero[r] << 16 : 0u), v);
+      spread<GP>(absent ? 0u : c.scale[r] | (ZERO ? c.zero[r] << 16 : 0u), v);
 #pragma unroll
       for (int j = 0; j < GP; ++j) {
         s[r][j] = __uint_as_float(v[j] << 16);
@@ -298,7 +295,8 @@ __global__ __launch_bounds__(W * 64) void w4_matvec_kernel(int64_t T, int K, con
 template <int XT, int TB, int R, int RW, int KW, int NS, int G, bool ZERO>
 __global__ __launch_bounds__(RW * KW * 64) void w4_matvec_shared_kernel(int64_t T, int K, const uint8_t* __restrict__ x,
                                                                         const float* __restrict__ x_scale,
-                                                                        const W4Table tab, int t_blocks, bool y_bf16) {
+                                                                        const W4Table tab, int t_blocks, bool y_bf16,
+                                                                        int splits, float* __restrict__ part) {
   using X = Rows<XT>;
   using Op = typename X::Op;
   using Acc = typename X::Acc;
@@ -313,12 +311,15 @@ __global__ __launch_bounds__(RW * KW * 64) void w4_matvec_shared_kernel(int64_t 
   __shared__ float sums[KW > 1 ? KW - 1 : 1][RW][R * TB * 4][64];
   const int lane = threadIdx.x & 63, l16 = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), rw = wave % RW, kw = wave / RW;
-  const int64_t t0 = static_cast<int64_t>(blockIdx.x % t_blocks) * (16 * TB);
-  int group = blockIdx.x / t_blocks, p = 0;
+  const int sp = blockIdx.x % splits;
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x / splits % t_blocks) * (16 * TB);
+  int group = blockIdx.x / splits / t_blocks, p = 0;
   while (group >= tab.group_end[p]) ++p;
   if (p > 0) group -= tab.group_end[p - 1];
   const int N = tab.N[p], nt = (N + 15) / 16, kt = (K + 127) / 128, kg = K / G;
-  const int steps = (kt + KW - 1) / KW;
+  // this workgroup's steps of KW chunks (the launcher leaves no split empty)
+  const int all_steps = (kt + KW - 1) / KW, per = (all_steps + splits - 1) / splits;
+  const int step0 = sp * per, steps = min(per, all_steps - step0);
   const int tile0 = (group * RW + rw) * R;
   __amdgpu_buffer_rsrc_t code_rs[R], scale_rs[R], zero_rs[R];
 #pragma unroll
@@ -348,9 +349,9 @@ __global__ __launch_bounds__(RW * KW * 64) void w4_matvec_shared_kernel(int64_t 
   auto load_x = [&](int i, unsigned char* stage) {
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
-      const int at = min(i * KW + copy_c[j] * 1024 / kChunk, kt - 1);
+      const int at = min((step0 + i) * KW + copy_c[j] * 1024 / kChunk, kt - 1);
       uint32_t off = copy_at[j];
-      // (in place of the half that a last chunk lacks, the first one; the step clears it)
+      // (in place of the half that a last chunk lacks, the first one; its scales become 0)
       if (has_half && at == kt - 1) off -= ((lane ^ (copy_c[j] * kCopyRows + lane / kPieces)) & (kPieces / 2)) * 16;
       buf_load16_lds(x_rs, stage + copy_c[j] * 1024, off, at * kRowBytes);
     }
@@ -361,7 +362,7 @@ __global__ __launch_bounds__(RW * KW * 64) void w4_matvec_shared_kernel(int64_t 
   };
   Chunk ring[NS];
   auto load_w = [&](int i, Chunk& c) {
-    const int at = min(i * KW + kw, kt - 1);
+    const int at = min((step0 + i) * KW + kw, kt - 1);
     const uint32_t ga = has_half && at == kt - 1 ? group_at_half : group_at;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
@@ -385,15 +386,15 @@ __global__ __launch_bounds__(RW * KW * 64) void w4_matvec_shared_kernel(int64_t 
     return *reinterpret_cast<const Op*>(chunk + row * kRowBytes + 16 * piece + (byte & 15));
   };
   auto step = [&](int i, const Chunk& c, const unsigned char* stage) {
-    const int at = i * KW + kw;
+    const int at = (step0 + i) * KW + kw;
     if (at >= kt) return;  // the last step may lack a chunk
-    const bool half = has_half && at == kt - 1;
+    const bool absent = has_half && at == kt - 1 && g >= 2;  // the lane's group
     const unsigned char* const chunk = stage + kw * kChunk;
     float s[R][GP], z[R][GP];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       uint32_t v[GP];
-      spread<GP>(c.scale[r] | (ZERO ? c.zero[r] << 16 : 0u), v);
+      spread<GP>(absent ? 0u : c.scale[r] | (ZERO ? c.zero[r] << 16 : 0u), v);
 #pragma unroll
       for (int j = 0; j < GP; ++j) {
         s[r][j] = __uint_as_float(v[j] << 16);
@@ -407,9 +408,7 @@ __global__ __launch_bounds__(RW * KW * 64) void w4_matvec_shared_kernel(int64_t 
       typename X::Wide xq[TB];
 #pragma unroll
       for (int b = 0; b < TB; ++b) {
-        Op o = x_op(chunk, b, q);
-        if (q >= 2 && half) o = Op{};
-        xq[b] = X::widen(o);
+        xq[b] = X::widen(x_op(chunk, b, q));
         xs[b] = X::mma(xq[b], minus, first ? Acc{} : xs[b]);
       }
 #pragma unroll
@@ -486,9 +485,9 @@ __global__ __launch_bounds__(RW * KW * 64) void w4_matvec_shared_kernel(int64_t 
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const int64_t t = min(t0 + 16 * b + 4 * g + e, T - 1);
-      factor[b][e] = x_scale != nullptr ? x_scale[t] : 1.f;
+      factor[b][e] = x_scale != nullptr && splits == 1 ? x_scale[t] : 1.f;
     }
-  auto finish = [&](auto* y) {
+  auto finish = [&](auto* y, int64_t stride) {
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       const int n = (tile0 + r) * 16 + l16;
@@ -503,70 +502,174 @@ __global__ __launch_bounds__(RW * KW * 64) void w4_matvec_shared_kernel(int64_t 
             for (int k = 0; k < KW - 1; ++k) v += sums[k][rw][(r * TB + b) * 4 + e][lane];
           v *= factor[b][e];
           if (t < T && n < N) {
-            if constexpr (sizeof(*y) == 2) y[t * N + n] = to_bf16(v);
-            else y[t * N + n] = v;
+            if constexpr (sizeof(*y) == 2) y[t * stride + n] = to_bf16(v);
+            else y[t * stride + n] = v;
           }
         }
     }
   };
-  if (y_bf16) finish(static_cast<uint16_t*>(tab.y[p]));
-  else finish(static_cast<float*>(tab.y[p]));
+  if (splits > 1) {
+    int64_t all = 0, before = 0;
+    for (int i = 0; i < tab.n; ++i) {
+      before = i == p ? all : before;
+      all += tab.N[i];
+    }
+    finish(part + sp * T * all + before, all);
+  } else if (y_bf16) {
+    finish(static_cast<uint16_t*>(tab.y[p]), N);
+  } else {
+    finish(static_cast<float*>(tab.y[p]), N);
+  }
 }
 
-// One launch for the table's group size and zero points: the kernel with K-split waves
-// (SHARED = 0: <XT, TB, R, W, D>) or the one with x in LDS (<XT, TB, R, RW, KW, NS = SHARED>).
-template <int XT, int TB, int R, int A, int B, int SHARED = 0>
-hipError_t run(int64_t T, int K, int group, const void* x, const float* x_scale, W4Table tab, bool y_bf16,
-               hipStream_t stream) {
+// y = x_scale sum over splits of part [splits][T][all outputs side by side], in order.
+__global__ __launch_bounds__(256) void w4_matvec_join_kernel(int64_t T, int64_t all, int splits,
+                                                             const float* __restrict__ part,
+                                                             const float* __restrict__ x_scale, const W4Table tab,
+                                                             bool y_bf16) {
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (i >= T * all) return;
+  float v = 0.f;
+  for (int k = 0; k < splits; ++k) v += part[k * T * all + i];
+  const int64_t t = i / all;
+  int64_t n = i - t * all;
+  int p = 0;
+  while (n >= tab.N[p]) n -= tab.N[p++];
+  if (x_scale != nullptr) v *= x_scale[t];
+  const int64_t at = t * tab.N[p] + n;
+  if (y_bf16) static_cast<uint16_t*>(tab.y[p])[at] = to_bf16(v);
+  else static_cast<float*>(tab.y[p])[at] = v;
+}
+
+// A call's arguments, as the launchers pass them on.
+struct Call {
+  int64_t T;
+  int K, group;
+  const void* x;
+  const float* x_scale;
+  W4Table tab;
+  bool y_bf16;
+  int splits;
+  float* part;
+  hipStream_t stream;
+};
+
+// The launch for the call's group size and zero points: the kernel with K-split waves
+// (SHARED = 0: <XT, TB, R, W, D>) or the one with x in LDS (<XT, TB, R, RW, KW>).
+template <int XT, int TB, int R, int A, int B, int SHARED>
+hipError_t run(Call c) {
   constexpr int kTiles = SHARED > 0 ? R * A : R;
   int groups = 0;
-  for (int p = 0; p < tab.n; ++p) {
-    groups += ((tab.N[p] + 15) / 16 + kTiles - 1) / kTiles;
-    tab.group_end[p] = groups;
+  for (int p = 0; p < c.tab.n; ++p) {
+    groups += ((c.tab.N[p] + 15) / 16 + kTiles - 1) / kTiles;
+    c.tab.group_end[p] = groups;
   }
-  const int t_blocks = static_cast<int>((T + 16 * TB - 1) / (16 * TB));
-  const dim3 grid(static_cast<unsigned>(groups) * static_cast<unsigned>(t_blocks));
-  const auto xb = static_cast<const uint8_t*>(x);
+  const int t_blocks = static_cast<int>((c.T + 16 * TB - 1) / (16 * TB));
+  const dim3 grid(static_cast<unsigned>(groups) * static_cast<unsigned>(t_blocks) * static_cast<unsigned>(c.splits));
+  const auto x = static_cast<const uint8_t*>(c.x);
   auto go = [&](auto g, auto zero) {
     constexpr int kG = decltype(g)::value;
     constexpr bool kZero = decltype(zero)::value;
     if constexpr (SHARED > 0)
-      w4_matvec_shared_kernel<XT, TB, R, A, B, SHARED, kG, kZero>
-          <<<grid, A * B * 64, 0, stream>>>(T, K, xb, x_scale, tab, t_blocks, y_bf16);
+      w4_matvec_shared_kernel<XT, TB, R, A, B, 3, kG, kZero>
+          <<<grid, A * B * 64, 0, c.stream>>>(c.T, c.K, x, c.x_scale, c.tab, t_blocks, c.y_bf16, c.splits, c.part);
     else
-      w4_matvec_kernel<XT, TB, R, A, B, kG, kZero><<<grid, A * 64, 0, stream>>>(T, K, xb, x_scale, tab, t_blocks, y_bf16);
+      w4_matvec_kernel<XT, TB, R, A, B, kG, kZero>
+          <<<grid, A * 64, 0, c.stream>>>(c.T, c.K, x, c.x_scale, c.tab, t_blocks, c.y_bf16);
   };
   auto with = [&](auto zero) {
-    if (group == 32) go(std::integral_constant<int, 32>{}, zero);
-    else if (group == 64) go(std::integral_constant<int, 64>{}, zero);
+    if (c.group == 32) go(std::integral_constant<int, 32>{}, zero);
+    else if (c.group == 64) go(std::integral_constant<int, 64>{}, zero);
     else go(std::integral_constant<int, 128>{}, zero);
   };
-  if (tab.zeros[0] != nullptr) with(std::true_type{});
+  if (c.tab.zeros[0] != nullptr) with(std::true_type{});
   else with(std::false_type{});
+  if (c.splits > 1) {
+    int64_t all = 0;
+    for (int p = 0; p < c.tab.n; ++p) all += c.tab.N[p];
+    w4_matvec_join_kernel<<<dim3(static_cast<unsigned>((c.T * all + 255) / 256)), 256, 0, c.stream>>>(
+        c.T, all, c.splits, c.part, c.x_scale, c.tab, c.y_bf16);
+  }
   return hipGetLastError();
 }
 
-template <int XT>
-hipError_t pick(int64_t T, int K, int group, const void* x, const float* x_scale, const W4Table& tab, bool y_bf16,
-                hipStream_t stream) {
-  int tiles = 0;
-  for (int p = 0; p < tab.n; ++p) tiles += (tab.N[p] + 15) / 16;
-  if (T <= 16) {
-    if (tiles <= 256) return run<XT, 1, 1, 16, 2>(T, K, group, x, x_scale, tab, y_bf16, stream);
-    if (tiles <= 768) return run<XT, 1, 2, 8, 2>(T, K, group, x, x_scale, tab, y_bf16, stream);
-    return run<XT, 1, 4, 8, 1>(T, K, group, x, x_scale, tab, y_bf16, stream);
+// Which kernel, and over how many workgroups d_in is split (their float32 sums meet in
+// the workspace and a second launch joins them, about 2 us). Measured (us):
+//   * up to 16 rows. Over 768 tiles there are workgroups enough: four tiles each (8192 ->
+//     28672 at 1 row 27; two tiles and 16 waves 32). Fewer tiles at a usual depth: two tiles
+//     over 16 waves (4096 -> 6144 at 4 rows 5.9; one tile 6.9), one tile below 257 (4096 ->
+//     1024 at 1 row 4.2; two 4.9). From 96 chunks with few tiles, x in LDS and d_in split
+//     (28672 -> 8192 at 16 rows 33, 28672 -> 1024 at 16 rows 14; two tiles over 16 waves 40
+//     and 18).
+//   * more rows. 32 or 64 in one block where 8-tile workgroups fill the GPU (5120 -> 32003
+//     at 64 rows 40; blocks of 32 rows 50), otherwise blocks of 32 rows, 4-tile workgroups
+//     and d_in split (28672 -> 2048 at 64 rows 24; 8-tile workgroups of 64 rows, split as
+//     often, 32; unsplit 59).
+enum Kind { kOneTile, kTwoTiles, kFourTiles, kDeep, kWide32, kWide64, kNarrow };
+struct Plan {
+  Kind kind;
+  int splits;
+};
+constexpr int kMaxSplits = 16;
+Plan plan(int64_t T, int64_t K, int n, const int* N) {
+  int64_t tiles = 0, groups4 = 0, groups8 = 0;
+  for (int p = 0; p < n; ++p) {
+    const int64_t t = (N[p] + 15) / 16;
+    tiles += t;
+    groups4 += (t + 3) / 4;
+    groups8 += (t + 7) / 8;
   }
-  if (T <= 32) return run<XT, 2, 2, 4, 2, 3>(T, K, group, x, x_scale, tab, y_bf16, stream);
-  return run<XT, 4, 2, 4, 2, 3>(T, K, group, x, x_scale, tab, y_bf16, stream);
+  const int64_t chunks = (K + 127) / 128;
+  // as many splits as give two workgroups a CU, each with four steps of kw chunks at least
+  auto split = [&](Kind kind, int64_t groups, int64_t kw) {
+    const int64_t steps = (chunks + kw - 1) / kw;
+    int64_t s = std::min<int64_t>({512 / groups, steps / 4, kMaxSplits});
+    if (s < 2) return Plan{kind, 1};
+    const int64_t per = (steps + s - 1) / s;
+    return Plan{kind, static_cast<int>((steps + per - 1) / per)};  // none empty
+  };
+  if (T <= 16) {
+    if (tiles > 768) return {kFourTiles, 1};
+    if (chunks >= 96) return split(kDeep, groups4, 4);
+    return {tiles > 256 ? kTwoTiles : kOneTile, 1};
+  }
+  const int64_t blocks32 = (T + 31) / 32, blocks64 = (T + 63) / 64;
+  if (T > 32 && groups8 * blocks64 >= 192) return {kWide64, 1};
+  if (groups8 * blocks32 >= 192) return {kWide32, 1};
+  return split(kNarrow, groups4 * blocks32, 2);
+}
+
+template <int XT>
+hipError_t pick(Kind kind, const Call& c) {
+  switch (kind) {
+    case kOneTile: return run<XT, 1, 1, 16, 2, 0>(c);
+    case kTwoTiles: return run<XT, 1, 2, 16, 2, 0>(c);
+    case kFourTiles: return run<XT, 1, 4, 8, 1, 0>(c);
+    case kDeep: return run<XT, 1, 1, 4, 4, 1>(c);
+    case kWide32: return run<XT, 2, 2, 4, 2, 1>(c);
+    case kWide64: return run<XT, 4, 2, 4, 2, 1>(c);
+    case kNarrow: return run<XT, 2, 1, 4, 2, 1>(c);
+  }
+  return hipErrorInvalidValue;
 }
 
 }  // namespace
 
+size_t w4_matvec_bytes(int64_t T, int64_t K, int n, const int* N) {
+  const Plan p = plan(T, K, n, N);
+  if (p.splits == 1) return 0;
+  int64_t all = 0;
+  for (int i = 0; i < n; ++i) all += N[i];
+  return (static_cast<size_t>(p.splits) * T * all * 4 + 255) / 256 * 256;
+}
+
 hipError_t launch_w4_matvec(int64_t T, int K, int group, int x_type, const void* x, const float* x_scale,
-                            const W4Table& tab, bool y_bf16, hipStream_t stream) {
-  if (x_type == kRowBf16) return pick<kRowBf16>(T, K, group, x, x_scale, tab, y_bf16, stream);
-  if (x_type == kRowE4m3) return pick<kRowE4m3>(T, K, group, x, x_scale, tab, y_bf16, stream);
-  return pick<kRowI8>(T, K, group, x, x_scale, tab, y_bf16, stream);
+                            const W4Table& tab, bool y_bf16, void* workspace, hipStream_t stream) {
+  const Plan p = plan(T, K, tab.n, tab.N);
+  const Call c{T, K, group, x, x_scale, tab, y_bf16, p.splits, static_cast<float*>(workspace), stream};
+  if (x_type == kRowBf16) return pick<kRowBf16>(p.kind, c);
+  if (x_type == kRowE4m3) return pick<kRowE4m3>(p.kind, c);
+  return pick<kRowI8>(p.kind, c);
 }
 
 }  // namespace lnf4

@@ -23,7 +23,8 @@ import torch
 from . import LN_BF16, LN_F32, LN_MAX_PROJ, LN_OK, LoraNF4Error, _SIGS, _workspace, library
 
 __all__ = ["rmsnorm_fwd", "rmsnorm_fwd_quant", "rmsnorm_bwd", "rmsnorm_bwd_workspace_bytes", "w4_quantize",
-           "w4_dequantize", "w4_matvec", "w4_matvec_multi", "NORM_W4_SYMBOLS", "LN_E4M3", "LN_I8"]
+           "w4_dequantize", "w4_matvec", "w4_matvec_multi", "w4_matvec_workspace_bytes",
+           "w4_matvec_multi_workspace_bytes", "NORM_W4_SYMBOLS", "LN_E4M3", "LN_I8"]
 
 LN_E4M3, LN_I8 = 2, 3
 
@@ -35,8 +36,10 @@ _NORM_W4_SIGS = {
     "rmsnorm_bwd_workspace_bytes": (ctypes.c_size_t, [_i64, _i64]),
     "w4_quantize": (_i, [_p, _i, _i64, _i64, _i32, _p, _p, _p, _p]),
     "w4_dequantize": (_i, [_p, _p, _p, _i64, _i64, _i32, _i, _p, _p]),
-    "w4_matvec": (_i, [_i64, _i64, _i64, _i32, _i, _p, _p, _p, _p, _p, _i, _p, _p]),
-    "w4_matvec_multi": (_i, [_i64, _i64, _i32, _p, _i32, _i, _p, _p, _p, _p, _p, _i, _p, _p]),
+    "w4_matvec": (_i, [_i64, _i64, _i64, _i32, _i, _p, _p, _p, _p, _p, _i, _p, _p, ctypes.c_size_t, _p]),
+    "w4_matvec_workspace_bytes": (ctypes.c_size_t, [_i64, _i64, _i64]),
+    "w4_matvec_multi": (_i, [_i64, _i64, _i32, _p, _i32, _i, _p, _p, _p, _p, _p, _i, _p, _p, ctypes.c_size_t, _p]),
+    "w4_matvec_multi_workspace_bytes": (ctypes.c_size_t, [_i64, _i64, _i32, _p]),
 }
 _SIGS.update(_NORM_W4_SIGS)
 NORM_W4_SYMBOLS = tuple(_NORM_W4_SIGS)
@@ -206,10 +209,20 @@ def _x_args(x, x_scale, dtype):
         _at(x_scale, "x_scale", dev, torch.float32, (x.shape[0],)), _code(_PLAIN, dtype, "dtype")
 
 
+def w4_matvec_workspace_bytes(T: int, d_in: int, d_out: int) -> int:
+    return int(library().w4_matvec_workspace_bytes(T, d_in, d_out))
+
+
+def w4_matvec_multi_workspace_bytes(T: int, d_in: int, d_outs) -> int:
+    widths = array("q", d_outs)
+    return int(library().w4_matvec_multi_workspace_bytes(T, d_in, len(widths), widths.buffer_info()[0]))
+
+
 def w4_matvec(x, codes, scales, zeros=None, *, d_out: int | None = None, x_scale=None, dtype=torch.bfloat16,
-              out=None):
+              out=None, workspace: torch.Tensor | None = None):
     """y = (x_scale x) W^T [T, d_out] in dtype (float32 or bf16) for x [T, d_in] bf16, float8_e4m3fn
-    or int8 and a packed weight; x_scale: float32 [T] or None. Made for up to 64 rows."""
+    or int8 and a packed weight; x_scale: float32 [T] or None. Made for up to 64 rows. A workspace is
+    allocated where one is needed (w4_matvec_workspace_bytes) and none is given."""
     dev, xt, xs, yt = _x_args(x, x_scale, dtype)
     T, K = x.shape
     N, group, c, s, z = _packed(codes, scales, zeros, K, d_out, dev)
@@ -218,13 +231,16 @@ def w4_matvec(x, codes, scales, zeros=None, *, d_out: int | None = None, x_scale
         y = out.data_ptr()
     else:
         y = _at(out, "out", dev, dtype, (T, N))
-    _call("w4_matvec", dev, T, K, N, group, xt, x.data_ptr(), xs, c, s, z, yt, y)
+    ws = _workspace(library().w4_matvec_workspace_bytes(T, K, N), workspace, x.device)
+    _call("w4_matvec", dev, T, K, N, group, xt, x.data_ptr(), xs, c, s, z, yt, y, None if ws is None else ws.data_ptr(),
+          0 if ws is None else ws.numel())
     return out
 
 
-def w4_matvec_multi(x, codes, scales, zeros=None, *, d_out=None, x_scale=None, dtype=torch.bfloat16):
-    """[y_g] of several packed weights (lists, one entry per weight) that read the same x, in one
-    launch: the same values as one w4_matvec each. zeros: None, or one entry per weight."""
+def w4_matvec_multi(x, codes, scales, zeros=None, *, d_out=None, x_scale=None, dtype=torch.bfloat16,
+                    workspace: torch.Tensor | None = None):
+    """[y_g] of several packed weights (lists, one entry per weight) that read the same x, as one
+    w4_matvec each but together in one launch. zeros: None, or one entry per weight."""
     dev, xt, xs, yt = _x_args(x, x_scale, dtype)
     T, K = x.shape
     n = len(codes)
@@ -241,6 +257,8 @@ def w4_matvec_multi(x, codes, scales, zeros=None, *, d_out=None, x_scale=None, d
     # the five arrays of the C call side by side (read during the call only)
     table = array("q", (*N, *c, *s, *z, *(y.data_ptr() for y in ys)))
     at, _ = table.buffer_info()
+    ws = _workspace(library().w4_matvec_multi_workspace_bytes(T, K, n, at), workspace, x.device)
     _call("w4_matvec_multi", dev, T, K, n, at, groups[0], xt, x.data_ptr(), xs, at + 8 * n, at + 16 * n,
-          at + 24 * n if z[0] else None, yt, at + 32 * n)
+          at + 24 * n if z[0] else None, yt, at + 32 * n, None if ws is None else ws.data_ptr(),
+          0 if ws is None else ws.numel())
     return ys

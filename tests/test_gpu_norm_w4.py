@@ -192,7 +192,10 @@ XT = {"bf16": BF, "e4m3": torch.float8_e4m3fn, "i8": torch.int8}
 MV = [(1, 64, 1, 32), (1, 64, 16, 64), (2, 128, 17, 128), (3, 192, 37, 64), (4, 4096, 100, 128), (5, 320, 33, 32),
       (8, 1024, 256, 64), (9, 960, 64, 64), (15, 2048, 48, 32), (16, 512, 300, 128), (17, 1152, 40, 128),
       (31, 448, 65, 32), (33, 256, 20, 64), (48, 1024, 129, 128), (64, 640, 130, 64), (65, 640, 31, 128),
-      (130, 192, 40, 64), (1, 28672, 48, 128), (3, 8256, 1040, 64), (16, 8192, 4100, 128), (1, 128, 9000, 32)]
+      (130, 192, 40, 64), (1, 28672, 48, 128), (3, 8256, 1040, 64), (16, 8192, 4100, 128), (1, 128, 9000, 32),
+      # d_in split across workgroups: uneven last splits, a half-filled last chunk, one tile
+      (2, 12480, 100, 64), (16, 13056, 530, 128), (11, 28672, 16, 32), (20, 1024, 40, 32), (40, 4288, 70, 64),
+      (64, 8192, 520, 128), (33, 4096, 3200, 128), (70, 1088, 33, 64), (24, 192, 24600, 64)]
 
 
 @pytest.mark.parametrize("kind", ["bf16", "e4m3", "i8"])
@@ -256,7 +259,7 @@ def test_w4_matvec_guard_bands(q):
         x = make(31, T, 256).cuda()
         buf = Guarded(T * N * 2)
         st = q.library().w4_matvec(T, 256, N, 64, 1, x.data_ptr(), None, codes.data_ptr(), scales.data_ptr(), None, 1,
-                                   buf.ptr, torch.cuda.current_stream().cuda_stream)
+                                   buf.ptr, None, 0, torch.cuda.current_stream().cuda_stream)
         assert st == 0 and buf.canaries_intact()
         assert torch.equal(buf.view(BF, (T, N)), q.w4_matvec(x, codes, scales, zeros, d_out=N))
 

@@ -108,8 +108,8 @@ def test_packing_refusals(lib, f):
     assert f(lib, c=at(0)) == (EALIAS)
 
 
-def mv(lib, T=2, K=192, N=40, g=64, xt=BF16, x=at(0), xs=None, c=at(1), s=at(2), z=None, yt=BF16, y=at(3)):
-    return lib.w4_matvec(T, K, N, g, xt, x, xs, c, s, z, yt, y, None)
+def mv(lib, T=2, K=192, N=40, g=64, xt=BF16, x=at(0), xs=None, c=at(1), s=at(2), z=None, yt=BF16, y=at(3), ws=None, nb=0):
+    return lib.w4_matvec(T, K, N, g, xt, x, xs, c, s, z, yt, y, ws, ctypes.c_size_t(nb), None)
 
 
 def test_matvec_refusals(lib):
@@ -121,11 +121,31 @@ def test_matvec_refusals(lib):
     assert mv(lib, T=0, x=None, y=None) == OK
 
 
+def test_matvec_workspace(lib):
+    """Only where d_in is split: deep weights of few tiles, or more rows than 16 on few tiles."""
+    need = lib.w4_matvec_workspace_bytes
+    assert need(1, 4096, 1024) == need(16, 8192, 28672) == need(64, 5120, 32000) == need(1, 28672, 16384) == 0
+    assert need(0, 28672, 1024) == need(1, 28672 + 32, 1024) == need(1, 28672, 0) == need((1 << 21) + 1, 64, 1) == 0
+    # 8 chunks of 128 are 4 steps of 2: not two splits of at least 4 steps each
+    assert need(20, 1024, 40) == 0
+    for T, K, N in [(16, 28672, 8192), (1, 28672, 1024), (64, 4096, 4096), (20, 2048, 40)]:
+        n = need(T, K, N)
+        assert n > 0 and n % 256 == 0 and n >= 2 * T * N * 4
+        call = dict(T=T, K=K, N=N)
+        assert mv(lib, **call) == mv(lib, **call, ws=at(6), nb=n - 1) == EWORKSPACE
+        assert mv(lib, **call, ws=at(6) + 16, nb=n) == EALIGN
+        assert mv(lib, **call, ws=at(1), nb=n) == mv(lib, **call, ws=at(3), nb=n) == EALIAS
+    two = (ctypes.c_int64 * 2)(1024, 512)
+    assert lib.w4_matvec_multi_workspace_bytes(16, 28672, 2, two) == need(16, 28672, 1536) > 0
+    assert lib.w4_matvec_multi_workspace_bytes(16, 28672, 0, two) == 0
+    assert lib.w4_matvec_multi_workspace_bytes(16, 28672, 2, None) == 0
+
+
 def test_matvec_multi_refusals(lib):
     def call(n=2, d_out=(40, 33), c=(at(1), at(2)), s=(at(3), at(4)), z=None, y=(at(5), at(6)), T=2):
         arr = lambda a: None if a is None else (ctypes.c_void_p * len(a))(*a)  # noqa: E731
         do = None if d_out is None else (ctypes.c_int64 * len(d_out))(*d_out)
-        return lib.w4_matvec_multi(T, 192, n, do, 64, BF16, at(0), None, arr(c), arr(s), arr(z), BF16, arr(y), None)
+        return lib.w4_matvec_multi(T, 192, n, do, 64, BF16, at(0), None, arr(c), arr(s), arr(z), BF16, arr(y), None, 0, None)
 
     assert call(n=0) == call(n=9) == call(d_out=None) == call(c=None) == call(y=None) == EINVAL
     assert call(c=(at(1), None)) == call(z=(at(7), None)) == call(y=(None, at(6))) == EINVAL
