@@ -168,7 +168,13 @@ __global__ __launch_bounds__((TPR < 256 ? 256 : TPR)) void rmsnorm_fwd_kernel(
   const int i0 = threadIdx.x % TPR;
   if (TPR < 256 && t >= T) return;  // (whole waves; no barrier follows at TPR = 64)
   const int64_t row = t * d;
-  Held<E> hv[NV], wv[NV];
+  // (at 8 vectors a thread the weight is read a second time rather than kept)
+  constexpr bool kKeep = NV <= 4;
+  Held<E> hv[NV], wv[kKeep ? NV : 1];
+  auto weight = [&](int v) {
+    const int at = (i0 + v * TPR) * kN;
+    return kKeep ? wv[kKeep ? v : 0] : load_vec(w + at, d - at);
+  };
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
     const int at = (i0 + v * TPR) * kN;
@@ -182,9 +188,9 @@ __global__ __launch_bounds__((TPR < 256 ? 256 : TPR)) void rmsnorm_fwd_kernel(
       rv[v] = load_vec(res + row + at, d - at);
     }
 #pragma unroll
-    for (int v = 0; v < NV; ++v) {
+    for (int v = 0; kKeep && v < NV; ++v) {
       const int at = (i0 + v * TPR) * kN;
-      wv[v] = load_vec(w + at, d - at);
+      wv[kKeep ? v : 0] = load_vec(w + at, d - at);
     }
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
@@ -197,20 +203,23 @@ __global__ __launch_bounds__((TPR < 256 ? 256 : TPR)) void rmsnorm_fwd_kernel(
     }
   } else {
 #pragma unroll
-    for (int v = 0; v < NV; ++v) {
+    for (int v = 0; kKeep && v < NV; ++v) {
       const int at = (i0 + v * TPR) * kN;
-      wv[v] = load_vec(w + at, d - at);
+      wv[kKeep ? v : 0] = load_vec(w + at, d - at);
     }
   }
   float s = 0.f, m = 0.f;
 #pragma unroll
-  for (int v = 0; v < NV; ++v)
+  for (int v = 0; v < NV; ++v) {
+    Held<E> wt{};
+    if constexpr (kQuant) wt = weight(v);
 #pragma unroll
     for (int j = 0; j < kN; ++j) {
       const float f = elem(hv[v], j);
       s += f * f;
-      if constexpr (kQuant) m = fmaxf(m, fabsf(f * elem(wv[v], j)));
+      if constexpr (kQuant) m = fmaxf(m, fabsf(f * elem(wt, j)));
     }
+  }
   row_reduce<TPR>(s, m, red);
   const float rstd = 1.0f / __builtin_sqrtf(s / static_cast<float>(d) + eps);
   if (i0 == 0 && rstd_out != nullptr) rstd_out[t] = rstd;
@@ -227,11 +236,12 @@ __global__ __launch_bounds__((TPR < 256 ? 256 : TPR)) void rmsnorm_fwd_kernel(
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
     const int at = (i0 + v * TPR) * kN, left = d - at;
+    Held<E> wt = weight(v);
     repack(hv[v]);
-    repack(wv[v]);
+    repack(wt);
     float f[kN];
 #pragma unroll
-    for (int j = 0; j < kN; ++j) f[j] = elem(hv[v], j) * rstd * elem(wv[v], j);
+    for (int j = 0; j < kN; ++j) f[j] = elem(hv[v], j) * rstd * elem(wt, j);
     if constexpr (kQuant) {
 #pragma unroll
       for (int j = 0; j < kN; ++j) f[j] = f[j] * up * inv;
@@ -310,12 +320,17 @@ __global__ __launch_bounds__(BLOCK) void rmsnorm_bwd_kernel(int64_t T, int d, co
   constexpr int kN = Vec<E>::kN, kSlots = BLOCK / TPR;
   __shared__ float2 red[BLOCK / 64];
   const int i0 = threadIdx.x % TPR, slot = threadIdx.x / TPR;
-  Held<E> wv[NV];
+  constexpr bool kKeep = NV <= 4;  // as in the forward
+  Held<E> wv[kKeep ? NV : 1];
 #pragma unroll
-  for (int v = 0; v < NV; ++v) {
+  for (int v = 0; kKeep && v < NV; ++v) {
     const int at = (i0 + v * TPR) * kN;
-    wv[v] = load_vec(w + at, d - at);
+    wv[kKeep ? v : 0] = load_vec(w + at, d - at);
   }
+  auto weight = [&](int v) {
+    const int at = (i0 + v * TPR) * kN;
+    return kKeep ? wv[kKeep ? v : 0] : load_vec(w + at, d - at);
+  };
   float acc[DW ? NV * kN : 1];
 #pragma unroll
   for (int j = 0; j < (DW ? NV * kN : 1); ++j) acc[j] = 0.f;
@@ -337,12 +352,13 @@ __global__ __launch_bounds__(BLOCK) void rmsnorm_bwd_kernel(int64_t T, int d, co
     float s = 0.f, unused = 0.f;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      repack(wv[v]);
+      Held<E> wt = weight(v);
+      repack(wt);
 #pragma unroll
       for (int j = 0; j < kN; ++j) {
         const float n = elem(hv[v], j) * rstd, g = elem(gv[v], j);
         if constexpr (DW) acc[v * kN + j] += g * n;
-        s += g * elem(wv[v], j) * n;
+        s += g * elem(wt, j) * n;
       }
     }
     if constexpr (TPR > 64) __syncthreads();  // the last row's red has been read
@@ -353,12 +369,13 @@ __global__ __launch_bounds__(BLOCK) void rmsnorm_bwd_kernel(int64_t T, int d, co
       const int at = (i0 + v * TPR) * kN, left = dd - at;
       repack(hv[v]);
       repack(gv[v]);
-      repack(wv[v]);
+      Held<E> wt = weight(v);
+      repack(wt);
       float f[kN];
 #pragma unroll
       for (int j = 0; j < kN; ++j) {
         const float n = elem(hv[v], j) * rstd;
-        f[j] = rstd * (elem(gv[v], j) * elem(wv[v], j) - n * c);
+        f[j] = rstd * (elem(gv[v], j) * elem(wt, j) - n * c);
       }
       if (dh != nullptr) {
         const Held<E> e = load_vec(dh + row + at, left);
@@ -443,8 +460,17 @@ __global__ __launch_bounds__(1024) void rmsnorm_dw_kernel(int blocks, int d, con
   __shared__ float red[32][33];
   const int c = threadIdx.x & 31, k = threadIdx.x >> 5, i = blockIdx.x * 32 + c;
   float s = 0.f;
-  if (i < d)
-    for (int b = k; b < blocks; b += 32) s += part[static_cast<int64_t>(b) * d + i];
+  if (i < d) {
+    int b = k;
+    for (; b + 7 * 32 < blocks; b += 8 * 32) {  // eight loads in flight
+      float v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = part[static_cast<int64_t>(b + 32 * j) * d + i];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s += v[j];
+    }
+    for (; b < blocks; b += 32) s += part[static_cast<int64_t>(b) * d + i];
+  }
   red[k][c] = s;
   __syncthreads();
   if (k == 0 && i < d) {
@@ -469,13 +495,13 @@ constexpr int kFewRows = 512;
 struct RowShape {
   int tpr, nv;  // tpr 0: does not fit
 };
-RowShape row_shape(int64_t T, int64_t vecs, int most) {
+RowShape row_shape(int64_t T, int64_t vecs, int most, int most1024) {
   const int nv64 = static_cast<int>((vecs + 63) / 64), nv256 = static_cast<int>((vecs + 255) / 256);
   const int nv1024 = static_cast<int>((vecs + 1023) / 1024);
-  auto up = [](int n) { return n <= 1 ? 1 : n <= 2 ? 2 : 4; };
+  auto up = [](int n) { return n <= 1 ? 1 : n <= 2 ? 2 : n <= 4 ? 4 : 8; };
   if (nv64 == 1 || (T > kFewRows && nv64 <= most)) return {64, up(nv64)};
   if (nv256 == 1 || (T > kFewRows && nv256 <= most)) return {256, up(nv256)};
-  if (nv1024 <= 4) return {1024, up(nv1024)};
+  if (nv1024 <= most1024) return {1024, up(nv1024)};
   return {0, 0};
 }
 
@@ -484,7 +510,7 @@ hipError_t fwd(int64_t T, int d, float eps, const void* xv, const void* rv, cons
                float* q_scale, float* rstd, hipStream_t stream) {
   const auto x = static_cast<const E*>(xv), res = static_cast<const E*>(rv), w = static_cast<const E*>(wv);
   const auto h = static_cast<E*>(hv);
-  const RowShape sh = row_shape(T, (d + Vec<E>::kN - 1) / Vec<E>::kN, 4);
+  const RowShape sh = row_shape(T, (d + Vec<E>::kN - 1) / Vec<E>::kN, 4, 32 / Vec<E>::kN);
   auto go = [&](auto tpr, auto nv) {
     constexpr int kTpr = decltype(tpr)::value, kNv = decltype(nv)::value, kRows = kTpr < 256 ? 256 / kTpr : 1;
     rmsnorm_fwd_kernel<E, OUT, kTpr, kNv><<<dim3(static_cast<unsigned>((T + kRows - 1) / kRows)), kTpr * kRows, 0, stream>>>(
@@ -494,7 +520,10 @@ hipError_t fwd(int64_t T, int d, float eps, const void* xv, const void* rv, cons
     switch (sh.nv) {
       case 1: go(tpr, std::integral_constant<int, 1>{}); break;
       case 2: go(tpr, std::integral_constant<int, 2>{}); break;
-      default: go(tpr, std::integral_constant<int, 4>{}); break;
+      case 4: go(tpr, std::integral_constant<int, 4>{}); break;
+      default:
+        if constexpr (decltype(tpr)::value == 1024 && sizeof(E) == 4) go(tpr, std::integral_constant<int, 8>{});
+        break;
     }
   };
   if (sh.tpr == 64) pick(std::integral_constant<int, 64>{});
@@ -528,7 +557,7 @@ hipError_t bwd(int64_t T, int d, const void* dyv, const void* dhv, const void* h
   const auto dx = static_cast<E*>(dxv), dw = static_cast<E*>(dwv);
   const auto part = static_cast<float*>(workspace);
   // (dw's sums take a register an element: 16 elements a thread leave four waves a SIMD)
-  const RowShape sh = row_shape(T, (d + Vec<E>::kN - 1) / Vec<E>::kN, dw != nullptr ? 16 / Vec<E>::kN : 4);
+  const RowShape sh = row_shape(T, (d + Vec<E>::kN - 1) / Vec<E>::kN, dw != nullptr ? 16 / Vec<E>::kN : 4, 32 / Vec<E>::kN);
   int blocks = bwd_blocks(T);
   auto go = [&](auto tpr, auto nv) {
     constexpr int kTpr = decltype(tpr)::value, kNv = decltype(nv)::value;
@@ -543,7 +572,10 @@ hipError_t bwd(int64_t T, int d, const void* dyv, const void* dhv, const void* h
     switch (sh.nv) {
       case 1: go(tpr, std::integral_constant<int, 1>{}); break;
       case 2: go(tpr, std::integral_constant<int, 2>{}); break;
-      default: go(tpr, std::integral_constant<int, 4>{}); break;
+      case 4: go(tpr, std::integral_constant<int, 4>{}); break;
+      default:
+        if constexpr (decltype(tpr)::value == 1024 && sizeof(E) == 4) go(tpr, std::integral_constant<int, 8>{});
+        break;
     }
   };
   if (sh.tpr == 64) pick(std::integral_constant<int, 64>{});

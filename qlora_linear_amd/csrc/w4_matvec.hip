@@ -522,23 +522,28 @@ __global__ __launch_bounds__(RW * KW * 64) void w4_matvec_shared_kernel(int64_t 
   }
 }
 
-// y = x_scale sum over splits of part [splits][T][all outputs side by side], in order.
-__global__ __launch_bounds__(256) void w4_matvec_join_kernel(int64_t T, int64_t all, int splits,
-                                                             const float* __restrict__ part,
+// y = x_scale sum over splits of part [splits][T][all outputs side by side], in order;
+// blockIdx.y: the row of x.
+constexpr int kMaxSplits = 16;
+__global__ __launch_bounds__(256) void w4_matvec_join_kernel(int64_t all, int splits, const float* __restrict__ part,
                                                              const float* __restrict__ x_scale, const W4Table tab,
                                                              bool y_bf16) {
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  if (i >= T * all) return;
+  const int64_t t = blockIdx.y, stride = gridDim.y * all;
+  int64_t n = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (n >= all) return;
+  const float* const at = part + t * all + n;
+  float w[kMaxSplits];
+#pragma unroll
+  for (int k = 0; k < kMaxSplits; ++k) w[k] = k < splits ? at[k * stride] : 0.f;
   float v = 0.f;
-  for (int k = 0; k < splits; ++k) v += part[k * T * all + i];
-  const int64_t t = i / all;
-  int64_t n = i - t * all;
+#pragma unroll
+  for (int k = 0; k < kMaxSplits; ++k) v += w[k];
+  if (x_scale != nullptr) v *= x_scale[t];
   int p = 0;
   while (n >= tab.N[p]) n -= tab.N[p++];
-  if (x_scale != nullptr) v *= x_scale[t];
-  const int64_t at = t * tab.N[p] + n;
-  if (y_bf16) static_cast<uint16_t*>(tab.y[p])[at] = to_bf16(v);
-  else static_cast<float*>(tab.y[p])[at] = v;
+  const int64_t o = t * tab.N[p] + n;
+  if (y_bf16) static_cast<uint16_t*>(tab.y[p])[o] = to_bf16(v);
+  else static_cast<float*>(tab.y[p])[o] = v;
 }
 
 // A call's arguments, as the launchers pass them on.
@@ -587,8 +592,8 @@ hipError_t run(Call c) {
   if (c.splits > 1) {
     int64_t all = 0;
     for (int p = 0; p < c.tab.n; ++p) all += c.tab.N[p];
-    w4_matvec_join_kernel<<<dim3(static_cast<unsigned>((c.T * all + 255) / 256)), 256, 0, c.stream>>>(
-        c.T, all, c.splits, c.part, c.x_scale, c.tab, c.y_bf16);
+    w4_matvec_join_kernel<<<dim3(static_cast<unsigned>((all + 255) / 256), static_cast<unsigned>(c.T)), 256, 0, c.stream>>>(
+        all, c.splits, c.part, c.x_scale, c.tab, c.y_bf16);
   }
   return hipGetLastError();
 }
@@ -610,7 +615,6 @@ struct Plan {
   Kind kind;
   int splits;
 };
-constexpr int kMaxSplits = 16;
 Plan plan(int64_t T, int64_t K, int n, const int* N) {
   int64_t tiles = 0, groups4 = 0, groups8 = 0;
   for (int p = 0; p < n; ++p) {

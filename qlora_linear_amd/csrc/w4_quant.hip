@@ -26,6 +26,17 @@ __device__ __forceinline__ void load8(const uint16_t* p, float (&v)[8]) {
   }
 }
 
+// rint of the float32 quotient v / s. The product with a reciprocal decides all but the
+// quotients near a half, where it may round to the other side; those (a lane in eight of
+// a wave, for bf16 weights) are divided. |v / s| <= 16, so the product is off by less
+// than 16 * 1.5 * 2^-23 < 2^-16.
+__device__ __forceinline__ float rint_quotient(float v, float s, float inv) {
+  const float t = v * inv;
+  float n = __builtin_rintf(t);
+  if (!(fabsf(fabsf(t - n) - 0.5f) > 0x1p-16f)) n = __builtin_rintf(__fdiv_rn(v, s));
+  return n;
+}
+
 // One 256-thread workgroup per tile. Thread t: row t >> 4, columns 8 (t & 15) .. + 7,
 // so a group is G / 8 consecutive lanes and its extrema a butterfly over them.
 template <typename In>
@@ -54,12 +65,14 @@ __global__ __launch_bounds__(kThreads) void w4_quantize_kernel(const In* __restr
   const bool asym = zeros != nullptr;
   const uint16_t sb = to_bf16(asym ? __fdiv_rn(__fsub_rn(hi, lo), 15.f) : __fdiv_rn(fmaxf(-lo, hi), 7.f));
   const float s = bf16_to_f32(sb);
+  // a scale whose reciprocal overflows makes t infinite or NaN below: divided as well
+  const float inv = __fdiv_rn(1.f, s);
   float z = 8.f;
-  if (asym) z = s > 0.f ? fminf(fmaxf(__builtin_rintf(__fdiv_rn(-lo, s)), 0.f), 15.f) : 0.f;
+  if (asym) z = s > 0.f ? fminf(fmaxf(rint_quotient(-lo, s, inv), 0.f), 15.f) : 0.f;
   uint32_t word = 0;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    const float c = s > 0.f ? fminf(fmaxf(__builtin_rintf(__fdiv_rn(v[j], s)) + z, 0.f), 15.f) : z;
+    const float c = s > 0.f ? fminf(fmaxf(rint_quotient(v[j], s, inv) + z, 0.f), 15.f) : z;
     word |= static_cast<uint32_t>(c) << (8 * (j & 3) + 4 * (j >> 2));
   }
   if (!ok) word = 0;

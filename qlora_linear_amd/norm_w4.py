@@ -20,13 +20,14 @@ from array import array
 
 import torch
 
-from . import LN_BF16, LN_F32, LN_MAX_PROJ, LN_OK, LoraNF4Error, _SIGS, _workspace, library
+from . import LN_BF16, LN_F32, LN_MAX_PROJ, LN_OK, LoraNF4Error, _SIGS, _dev, _workspace, library
 
 __all__ = ["rmsnorm_fwd", "rmsnorm_fwd_quant", "rmsnorm_bwd", "rmsnorm_bwd_workspace_bytes", "w4_quantize",
            "w4_dequantize", "w4_matvec", "w4_matvec_multi", "w4_matvec_workspace_bytes",
            "w4_matvec_multi_workspace_bytes", "NORM_W4_SYMBOLS", "LN_E4M3", "LN_I8"]
 
 LN_E4M3, LN_I8 = 2, 3
+LN_EWORKSPACE = -5
 
 _p, _i, _i64, _i32, _f = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_int32, ctypes.c_float
 _NORM_W4_SIGS = {
@@ -85,15 +86,33 @@ def _at(t, name, dev, dtype, shape):
     raise ValueError(f"{name} must be contiguous")
 
 
-def _call(name, dev, *args):
-    """The C entry point on the current stream of device `dev` (made the current device
-    for the launch, where it is not)."""
+def _status(name, dev, args):
+    """The C entry point's status, called on the current stream of device `dev` (made the
+    current device for the launch, where it is not)."""
     fn = getattr(library(), name)
     if torch._C._cuda_getDevice() == dev:
-        st = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
+        return fn(*args, torch._C._cuda_getCurrentRawStream(dev))
+    with torch.cuda.device(dev):
+        return fn(*args, torch._C._cuda_getCurrentRawStream(dev))
+
+
+def _call(name, dev, *args):
+    st = _status(name, dev, args)
+    if st != LN_OK:
+        raise LoraNF4Error(name, st)
+
+
+def _call_matvec(name, dev, args, workspace, need, x):
+    """A product on the caller's workspace, or on a new one of need() bytes where it turns out
+    that one is needed (most shapes take none, and asking costs as much as trying)."""
+    if workspace is None:
+        st = _status(name, dev, (*args, None, 0))
+        if st == LN_EWORKSPACE:
+            workspace = x.new_empty(need(), dtype=torch.uint8)
+            st = _status(name, dev, (*args, workspace.data_ptr(), workspace.numel()))
     else:
-        with torch.cuda.device(dev):
-            st = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
+        _dev(workspace, "workspace", torch.uint8)
+        st = _status(name, dev, (*args, workspace.data_ptr(), workspace.numel()))
     if st != LN_OK:
         raise LoraNF4Error(name, st)
 
@@ -231,9 +250,8 @@ def w4_matvec(x, codes, scales, zeros=None, *, d_out: int | None = None, x_scale
         y = out.data_ptr()
     else:
         y = _at(out, "out", dev, dtype, (T, N))
-    ws = _workspace(library().w4_matvec_workspace_bytes(T, K, N), workspace, x.device)
-    _call("w4_matvec", dev, T, K, N, group, xt, x.data_ptr(), xs, c, s, z, yt, y, None if ws is None else ws.data_ptr(),
-          0 if ws is None else ws.numel())
+    _call_matvec("w4_matvec", dev, (T, K, N, group, xt, x.data_ptr(), xs, c, s, z, yt, y), workspace,
+                 lambda: w4_matvec_workspace_bytes(T, K, N), x)
     return out
 
 
@@ -257,8 +275,7 @@ def w4_matvec_multi(x, codes, scales, zeros=None, *, d_out=None, x_scale=None, d
     # the five arrays of the C call side by side (read during the call only)
     table = array("q", (*N, *c, *s, *z, *(y.data_ptr() for y in ys)))
     at, _ = table.buffer_info()
-    ws = _workspace(library().w4_matvec_multi_workspace_bytes(T, K, n, at), workspace, x.device)
-    _call("w4_matvec_multi", dev, T, K, n, at, groups[0], xt, x.data_ptr(), xs, at + 8 * n, at + 16 * n,
-          at + 24 * n if z[0] else None, yt, at + 32 * n, None if ws is None else ws.data_ptr(),
-          0 if ws is None else ws.numel())
+    _call_matvec("w4_matvec_multi", dev, (T, K, n, at, groups[0], xt, x.data_ptr(), xs, at + 8 * n, at + 16 * n,
+                                          at + 24 * n if z[0] else None, yt, at + 32 * n), workspace,
+                 lambda: w4_matvec_multi_workspace_bytes(T, K, N), x)
     return ys
