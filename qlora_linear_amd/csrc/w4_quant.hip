@@ -26,19 +26,39 @@ __device__ __forceinline__ void load8(const uint16_t* p, float (&v)[8]) {
   }
 }
 
-// rint of the float32 quotient v / s. The product with a reciprocal decides all but the
-// quotients near a half, where it may round to the other side; those (a lane in eight of
-// a wave, for bf16 weights) are divided. |v / s| <= 16, so the product is off by less
-// than 16 * 1.5 * 2^-23 < 2^-16.
+// rint of the float32 quotient v / s, |v / s| <= 16. The product with the reciprocal
+// (1 ulp: off by less than 16 * 2^-22) decides all but the quotients near a half, where it
+// may lie on the other side; those (a lane in eight of a wave, for bf16 weights) are
+// divided, as are all of a scale whose reciprocal overflows (the comparison is then false).
 __device__ __forceinline__ float rint_quotient(float v, float s, float inv) {
-  const float t = v * inv;
-  float n = __builtin_rintf(t);
-  if (!(fabsf(fabsf(t - n) - 0.5f) > 0x1p-16f)) n = __builtin_rintf(__fdiv_rn(v, s));
+  constexpr float kMagic = 12582912.f;  // 1.5 * 2^23: the sum's last bit is 1
+  float n = __builtin_fmaf(v, inv, kMagic) - kMagic;
+  if (!(fabsf(__builtin_fmaf(v, inv, -n)) < 0.5f - 0x1p-16f)) n = __builtin_rintf(__fdiv_rn(v, s));
   return n;
 }
 
+// Minimum and maximum over the 4, 8 or 16 consecutive lanes of a group, by lane moves
+// inside a row of 16: neighbours, then pairs, are exchanged; after that quads hold one
+// value each and mirrors join them.
+template <int CTRL>
+__device__ __forceinline__ void join_extrema(float& lo, float& hi) {
+  auto moved = [](float v) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xF, 0xF, true));
+  };
+  lo = fminf(lo, moved(lo));
+  hi = fmaxf(hi, moved(hi));
+}
+__device__ __forceinline__ void group_extrema(int group, float& lo, float& hi) {
+  join_extrema<0xB1>(lo, hi);                     // quad_perm 1 0 3 2
+  join_extrema<0x4E>(lo, hi);                     // quad_perm 2 3 0 1
+  if (group >= 64) join_extrema<0x141>(lo, hi);   // row_half_mirror
+  if (group >= 128) join_extrema<0x140>(lo, hi);  // row_mirror
+}
+
 // One 256-thread workgroup per tile. Thread t: row t >> 4, columns 8 (t & 15) .. + 7,
-// so a group is G / 8 consecutive lanes and its extrema a butterfly over them.
+// so a group is G / 8 consecutive lanes. Bound by its arithmetic rather than by HBM
+// (about 14 instructions an element): one division a thread, the codes put together as
+// floats (sums of multiples of powers of 16 below 2^16 are exact), two conversions a word.
 template <typename In>
 __global__ __launch_bounds__(kThreads) void w4_quantize_kernel(const In* __restrict__ w, int64_t N, int64_t K,
                                                                int kt, int group, uint32_t* __restrict__ codes,
@@ -58,23 +78,21 @@ __global__ __launch_bounds__(kThreads) void w4_quantize_kernel(const In* __restr
     lo = fminf(lo, v[j]);
     hi = fmaxf(hi, v[j]);
   }
-  for (int o = group >> 4; o >= 1; o >>= 1) {
-    lo = fminf(lo, __shfl_xor(lo, o));
-    hi = fmaxf(hi, __shfl_xor(hi, o));
-  }
+  group_extrema(group, lo, hi);
   const bool asym = zeros != nullptr;
   const uint16_t sb = to_bf16(asym ? __fdiv_rn(__fsub_rn(hi, lo), 15.f) : __fdiv_rn(fmaxf(-lo, hi), 7.f));
   const float s = bf16_to_f32(sb);
-  // a scale whose reciprocal overflows makes t infinite or NaN below: divided as well
-  const float inv = __fdiv_rn(1.f, s);
+  const float inv = __builtin_amdgcn_rcpf(s);
   float z = 8.f;
   if (asym) z = s > 0.f ? fminf(fmaxf(rint_quotient(-lo, s, inv), 0.f), 15.f) : 0.f;
-  uint32_t word = 0;
+  float half[2] = {0.f, 0.f};  // the word's two halves
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    const float c = s > 0.f ? fminf(fmaxf(rint_quotient(v[j], s, inv) + z, 0.f), 15.f) : z;
-    word |= static_cast<uint32_t>(c) << (8 * (j & 3) + 4 * (j >> 2));
+    const float n = s > 0.f ? rint_quotient(v[j], s, inv) : 0.f;
+    const float c = __builtin_amdgcn_fmed3f(n + z, 0.f, 15.f);
+    half[(j & 3) >> 1] += c * static_cast<float>(1 << (8 * (j & 1) + 4 * (j >> 2)));
   }
+  uint32_t word = static_cast<uint32_t>(half[0]) | static_cast<uint32_t>(half[1]) << 16;
   if (!ok) word = 0;
   const int q = c8 >> 2, g = c8 & 3;
   codes[tile * 256 + 64 * g + 4 * r + q] = word;
