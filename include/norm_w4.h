@@ -82,8 +82,8 @@ size_t rmsnorm_bwd_workspace_bytes(int64_t T, int64_t d);
 /*
  * The packed 4-bit weight. A weight of d_out rows and d_in columns is held as
  *     w[n][k] = (c[n][k] - z[n][k / group]) s[n][k / group],   c, z in 0 .. 15
- * with group 32, 64 or 128, d_in a multiple of 64 and of group, any d_out >= 1. z is 8
- * everywhere where no zero points are stored. Codes lie in tiles of 16 rows x 128
+ * with group 32, 64 or 128, d_in a multiple of 64 and of group, any d_out >= 1, fewer than
+ * 2^24 tiles in all (see below). z is 8 everywhere where no zero points are stored. Codes lie in tiles of 16 rows x 128
  * columns, so that one wave reads a tile as 1024 consecutive bytes and each lane's 16
  * bytes are matrix-instruction operands in place:
  *   codes   uint8 [ceil(d_out / 16)][ceil(d_in / 128)][1024]; byte 256 g + 16 r + 4 q + i
@@ -119,7 +119,8 @@ int w4_dequantize(const uint8_t* codes, const uint16_t* scales, const uint8_t* z
  *   workspace w4_matvec_workspace_bytes(T, d_in, d_out) bytes (0 unless d_in is split
  *             across workgroups, where the float32 sums of the splits meet in it, added in
  *             a fixed order); may be NULL when that is 0
- * 0 <= T <= 2^21; made for up to 64 rows, where reading the packed weight bounds it. More
+ *             (two calls that may run at the same time need a workspace each)
+ * 0 <= T <= 2^21, T d_out <= 2^35 - 16 T; made for up to 64 rows, where reading the packed weight bounds it. More
  * rows run as blocks of 64, each reading the weight again.
  */
 int w4_matvec(int64_t T, int64_t d_in, int64_t d_out, int32_t group, int x_dtype, const void* x,

@@ -16,7 +16,6 @@ using namespace lnf4;
 bool plain_type(int t) { return t == LN_F32 || t == LN_BF16; }
 size_t type_bytes(int t) { return t == LN_F32 ? 4 : t == LN_BF16 ? 2 : 1; }
 
-// The rows of a norm: one workgroup each, so their number is bounded by a launch's.
 int check_norm(int64_t T, int64_t d, int dtype, float eps) {
   if (T < 0 || d < 1 || !plain_type(dtype) || !std::isfinite(eps) || !(eps > 0.f)) return LN_EINVAL;
   if (T > kMaxDim || d > LN_NORM_MAX_D) return LN_ESHAPE;
@@ -50,10 +49,12 @@ int check_w4(int64_t N, int64_t K, int32_t group) {
   if (N < 1 || K < 1) return LN_EINVAL;
   if (group != 32 && group != 64 && group != 128) return LN_ESHAPE;
   if (K % 64 != 0 || K % group != 0 || N > kMaxDim - 15 || K > LN_W4_MAX_D_IN) return LN_ESHAPE;
-  if ((N + 15) / 16 * ((K + 127) / 128) > (int64_t(1) << 30)) return LN_ESHAPE;
+  // a launch has fewer than 2^32 threads along x: 256 a tile when packing
+  if ((N + 15) / 16 * ((K + 127) / 128) >= (int64_t(1) << 24)) return LN_ESHAPE;
   return LN_OK;
 }
-constexpr int64_t kMaxW4Rows = int64_t(1) << 21;  // rows of x (the grid stays below 2^31 workgroups)
+constexpr int64_t kMaxW4Rows = int64_t(1) << 21;
+constexpr int64_t kMaxW4Outputs = int64_t(1) << 35;  // of one launch (one thread to 16 of them at least)
 size_t w4_code_bytes(int64_t N, int64_t K) { return static_cast<size_t>((N + 15) / 16 * ((K + 127) / 128)) * 1024; }
 size_t w4_groups(int64_t N, int64_t K, int32_t group) { return static_cast<size_t>((N + 15) / 16 * (K / group)) * 16; }
 
@@ -165,7 +166,7 @@ int w4_matvec_multi(int64_t T, int64_t d_in, int32_t n_proj, const int64_t* d_ou
     const uint8_t* z = zeros == nullptr ? nullptr : zeros[g];
     if (!aligned16(codes[g]) || !aligned16(scales[g]) || !aligned16(z) || !aligned16(y[g])) return LN_EALIGN;
     tiles += (d_out[g] + 15) / 16;
-    if (tiles > (int64_t(1) << 27)) return LN_ESHAPE;
+    if (tiles >= (int64_t(1) << 24)) return LN_ESHAPE;
     tab.N[g] = static_cast<int>(d_out[g]);
     tab.codes[g] = codes[g];
     tab.scales[g] = scales[g];
@@ -177,7 +178,7 @@ int w4_matvec_multi(int64_t T, int64_t d_in, int32_t n_proj, const int64_t* d_ou
     ins[n_in++] = {scales[g], gs * 2};
     ins[n_in++] = {z, gs};
   }
-  if (T > kMaxW4Rows) return LN_ESHAPE;
+  if (T > kMaxW4Rows || T * 16 * tiles > kMaxW4Outputs) return LN_ESHAPE;
   if (T == 0) return LN_OK;
   if (!aligned16(x) || !aligned16(x_scale)) return LN_EALIGN;
   const size_t need = w4_matvec_bytes(T, d_in, n_proj, tab.N);

@@ -154,6 +154,15 @@ __device__ __forceinline__ void row_reduce(float& s, float& m, float2* red) {
   }
 }
 
+// Workgroups of one row (or a few) each: a launch has fewer than 2^32 threads along x, so
+// many rows spread over y as well.
+constexpr int64_t kGridX = 1 << 20;
+dim3 row_grid(int64_t n) {
+  return n <= kGridX ? dim3(static_cast<unsigned>(n))
+                     : dim3(static_cast<unsigned>(kGridX), static_cast<unsigned>((n + kGridX - 1) / kGridX));
+}
+__device__ __forceinline__ int64_t row_block() { return static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x; }
+
 constexpr float kTiny = 0x1p-100f, kUp = 0x1p64f;
 
 // ---- forward ---------------------------------------------------------------------------
@@ -164,9 +173,9 @@ __global__ __launch_bounds__((TPR < 256 ? 256 : TPR)) void rmsnorm_fwd_kernel(
   constexpr int kN = Vec<E>::kN, kBlock = TPR < 256 ? 256 : TPR;
   constexpr bool kQuant = OUT == kRowE4m3 || OUT == kRowI8;
   __shared__ float2 red[kBlock / 64];
-  const int64_t t = static_cast<int64_t>(blockIdx.x) * (kBlock / TPR) + threadIdx.x / TPR;
+  const int64_t t = row_block() * (kBlock / TPR) + threadIdx.x / TPR;
   const int i0 = threadIdx.x % TPR;
-  if (TPR < 256 && t >= T) return;  // (whole waves; no barrier follows at TPR = 64)
+  if (t >= T) return;  // (whole rows; a workgroup with a barrier ahead has one row)
   const int64_t row = t * d;
   // (at 8 vectors a thread the weight is read a second time rather than kept)
   constexpr bool kKeep = NV <= 4;
@@ -267,14 +276,15 @@ __global__ __launch_bounds__((TPR < 256 ? 256 : TPR)) void rmsnorm_fwd_kernel(
 // time mostly from L2 (h is formed again from x and the residual).
 constexpr int kLoop = 1024;
 template <typename E, int OUT>
-__global__ __launch_bounds__(kLoop) void rmsnorm_fwd_loop_kernel(int d, float eps, const E* __restrict__ x,
+__global__ __launch_bounds__(kLoop) void rmsnorm_fwd_loop_kernel(int64_t T, int d, float eps, const E* __restrict__ x,
                                                                  const E* __restrict__ res,
                                                                  const E* __restrict__ w, E* __restrict__ h,
                                                                  void* __restrict__ y,
                                                                  float* __restrict__ q_scale,
                                                                  float* __restrict__ rstd_out) {
   __shared__ float2 red[kLoop / 64];
-  const int64_t t = blockIdx.x, row = t * d;
+  const int64_t t = row_block(), row = t * d;
+  if (t >= T) return;
   auto h_at = [&](int i) {
     const float v = to_f32(x[row + i]);
     return res == nullptr ? v : to_f32(from_f32<E>(v + to_f32(res[row + i])));
@@ -419,14 +429,15 @@ __global__ __launch_bounds__(BLOCK) void rmsnorm_bwd_kernel(int64_t T, int d, co
 
 // Rows wider than the registers hold: read twice.
 template <typename E>
-__global__ __launch_bounds__(kLoop) void rmsnorm_bwd_loop_kernel(int d, const E* __restrict__ dy,
+__global__ __launch_bounds__(kLoop) void rmsnorm_bwd_loop_kernel(int64_t T, int d, const E* __restrict__ dy,
                                                                  const E* __restrict__ dh,
                                                                  const E* __restrict__ h, const E* __restrict__ w,
                                                                  const float* __restrict__ rstd_in,
                                                                  E* __restrict__ dx) {
   __shared__ float2 red[kLoop / 64];
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * d;
-  const float rstd = rstd_in[blockIdx.x];
+  const int64_t t = row_block(), row = t * d;
+  if (t >= T) return;
+  const float rstd = rstd_in[t];
   float s = 0.f, unused = 0.f;
   for (int i = threadIdx.x; i < d; i += kLoop)
     s += to_f32(dy[row + i]) * to_f32(w[i]) * (to_f32(h[row + i]) * rstd);
@@ -513,7 +524,7 @@ hipError_t fwd(int64_t T, int d, float eps, const void* xv, const void* rv, cons
   const RowShape sh = row_shape(T, (d + Vec<E>::kN - 1) / Vec<E>::kN, 4, 32 / Vec<E>::kN);
   auto go = [&](auto tpr, auto nv) {
     constexpr int kTpr = decltype(tpr)::value, kNv = decltype(nv)::value, kRows = kTpr < 256 ? 256 / kTpr : 1;
-    rmsnorm_fwd_kernel<E, OUT, kTpr, kNv><<<dim3(static_cast<unsigned>((T + kRows - 1) / kRows)), kTpr * kRows, 0, stream>>>(
+    rmsnorm_fwd_kernel<E, OUT, kTpr, kNv><<<row_grid((T + kRows - 1) / kRows), kTpr * kRows, 0, stream>>>(
         T, d, eps, x, res, w, h, y, q_scale, rstd);
   };
   auto pick = [&](auto tpr) {
@@ -530,7 +541,7 @@ hipError_t fwd(int64_t T, int d, float eps, const void* xv, const void* rv, cons
   else if (sh.tpr == 256) pick(std::integral_constant<int, 256>{});
   else if (sh.tpr == 1024) pick(std::integral_constant<int, 1024>{});
   else
-    rmsnorm_fwd_loop_kernel<E, OUT><<<dim3(static_cast<unsigned>(T)), kLoop, 0, stream>>>(d, eps, x, res, w, h, y,
+    rmsnorm_fwd_loop_kernel<E, OUT><<<row_grid(T), kLoop, 0, stream>>>(T, d, eps, x, res, w, h, y,
                                                                                           q_scale, rstd);
   return hipGetLastError();
 }
@@ -582,7 +593,7 @@ hipError_t bwd(int64_t T, int d, const void* dyv, const void* dhv, const void* h
   else if (sh.tpr == 256) pick(std::integral_constant<int, 256>{});
   else if (sh.tpr == 1024) pick(std::integral_constant<int, 1024>{});
   else {
-    rmsnorm_bwd_loop_kernel<E><<<dim3(static_cast<unsigned>(T)), kLoop, 0, stream>>>(d, dy, dh, h, w, rstd, dx);
+    rmsnorm_bwd_loop_kernel<E><<<row_grid(T), kLoop, 0, stream>>>(T, d, dy, dh, h, w, rstd, dx);
     if (dw != nullptr) {
       blocks = std::min(blocks, 64);
       rmsnorm_dw_part_kernel<E><<<dim3((d + 255) / 256, blocks), 256, 0, stream>>>(T, d, dy, h, rstd, part);

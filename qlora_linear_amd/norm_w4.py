@@ -192,21 +192,36 @@ def w4_quantize(w, group: int = 128, zero_points: bool = False):
     return codes, scales, zeros
 
 
-def _packed(codes, scales, zeros, d_in, d_out, dev, tag=""):
-    """(d_out, group, addresses) of a packed weight whose rows are d_in wide."""
-    if not isinstance(scales, torch.Tensor) or scales.dim() != 3:
+def _packed(codes, scales, zeros, d_in, d_out, dev, index=None):
+    """(d_out, group, addresses) of a packed weight whose rows are d_in wide; index: its
+    place in a list, for errors."""
+    try:
+        nt, kg, rows = scales.shape
+        group = d_in // kg
+        n = 16 * nt if d_out is None else d_out
+        if rows == 16 and group in _GROUPS and kg * group == d_in and 16 * (nt - 1) < n <= 16 * nt and \
+                scales.dtype is torch.bfloat16 and scales.get_device() == dev and scales.is_contiguous() and \
+                codes.dtype is torch.uint8 and codes.shape == (nt, (d_in + 127) // 128, 1024) and \
+                codes.get_device() == dev and codes.is_contiguous():
+            if zeros is None:
+                return n, group, codes.data_ptr(), scales.data_ptr(), 0
+            if zeros.dtype is torch.uint8 and zeros.shape == (nt, kg, 16) and zeros.get_device() == dev and \
+                    zeros.is_contiguous():
+                return n, group, codes.data_ptr(), scales.data_ptr(), zeros.data_ptr()
+    except (AttributeError, TypeError, ValueError, ZeroDivisionError):
+        pass  # something else than such tensors: refused below
+    tag = "" if index is None else f"[{index}]"
+    if not isinstance(scales, torch.Tensor) or scales.dim() != 3 or scales.shape[2] != 16 or not scales.shape[1]:
         raise ValueError(f"scales{tag} must be [ceil(d_out / 16), d_in / group, 16]")
-    nt, kg, _ = shape = scales.shape
-    group = d_in // kg if kg else 0
-    if kg * group != d_in or group not in _GROUPS:
+    nt, kg, _ = scales.shape
+    if kg * (d_in // kg) != d_in or d_in // kg not in _GROUPS:
         raise ValueError(f"scales{tag} hold {kg} groups of a row: d_in {d_in} makes no group of 32, 64 or 128")
-    if d_out is None:
-        d_out = 16 * nt
-    elif not 16 * (nt - 1) < d_out <= 16 * nt:
+    if d_out is not None and not 16 * (nt - 1) < d_out <= 16 * nt:
         raise ValueError(f"d_out{tag} {d_out} does not fit scales{tag} of {nt} tiles of 16 rows")
-    c = _at(codes, f"codes{tag}", dev, torch.uint8, (nt, (d_in + 127) // 128, 1024))
-    s = _at(scales, f"scales{tag}", dev, torch.bfloat16, (nt, kg, 16))
-    return d_out, group, c, s, 0 if zeros is None else _at(zeros, f"zeros{tag}", dev, torch.uint8, shape)
+    _at(scales, f"scales{tag}", dev, torch.bfloat16, (nt, kg, 16))
+    _at(codes, f"codes{tag}", dev, torch.uint8, (nt, (d_in + 127) // 128, 1024))
+    _at(zeros, f"zeros{tag}", dev, torch.uint8, (nt, kg, 16))
+    raise ValueError(f"packed weight{tag} not understood")
 
 
 def w4_dequantize(codes, scales, zeros=None, *, d_out: int | None = None, d_in: int | None = None,
@@ -266,7 +281,7 @@ def w4_matvec_multi(x, codes, scales, zeros=None, *, d_out=None, x_scale=None, d
             (d_out is not None and len(d_out) != n):
         raise ValueError(f"codes, scales (zeros, d_out) must be lists of the same length, 1 to {LN_MAX_PROJ}")
     N, groups, c, s, z = zip(*(_packed(codes[g], scales[g], None if zeros is None else zeros[g], K,
-                                       None if d_out is None else d_out[g], dev, f"[{g}]") for g in range(n)))
+                                       None if d_out is None else d_out[g], dev, g) for g in range(n)))
     if len(set(groups)) > 1:
         raise ValueError("all weights must share the group size")
     if not all(z) and any(z):

@@ -195,7 +195,9 @@ MV = [(1, 64, 1, 32), (1, 64, 16, 64), (2, 128, 17, 128), (3, 192, 37, 64), (4, 
       (130, 192, 40, 64), (1, 28672, 48, 128), (3, 8256, 1040, 64), (16, 8192, 4100, 128), (1, 128, 9000, 32),
       # d_in split across workgroups: uneven last splits, a half-filled last chunk, one tile
       (2, 12480, 100, 64), (16, 13056, 530, 128), (11, 28672, 16, 32), (20, 1024, 40, 32), (40, 4288, 70, 64),
-      (64, 8192, 520, 128), (33, 4096, 3200, 128), (70, 1088, 33, 64), (24, 192, 24600, 64)]
+      (64, 8192, 520, 128), (33, 4096, 3200, 128), (70, 1088, 33, 64), (24, 192, 24600, 64),
+      # four tiles a workgroup; blocks of 64 rows, the last one short
+      (3, 192, 12400, 64), (16, 256, 12500, 128), (200, 128, 6500, 32), (64, 320, 24700, 64)]
 
 
 @pytest.mark.parametrize("kind", ["bf16", "e4m3", "i8"])
@@ -249,6 +251,55 @@ def test_w4_matvec_multi_equals_single(q, T, kind):
     ys = q.w4_matvec_multi(x, [w[0] for w in ws], [w[1] for w in ws], [w[2] for w in ws], d_out=widths, x_scale=scale)
     for w, n, y in zip(ws, widths, ys):
         assert torch.equal(y, q.w4_matvec(x, *w[:3], d_out=n, x_scale=scale)) and y.shape == (T, n)
+
+
+def test_w4_matvec_repeats_and_takes_a_workspace(q):
+    """d_in split across workgroups: the same bits each time, on the caller's workspace or not,
+    and from two streams at once (a workspace each)."""
+    T, K, N = 5, 16384, 200
+    codes, scales, zeros, _ = packed(62, N, K, 64, True)
+    x = make(34, T, K).cuda()
+    need = q.w4_matvec_workspace_bytes(T, K, N)
+    assert need > 0
+    want = q.w4_matvec(x, codes, scales, zeros, d_out=N, dtype=F)
+    ws = torch.full((need,), 255, dtype=torch.uint8, device="cuda")
+    for _ in range(3):
+        assert torch.equal(q.w4_matvec(x, codes, scales, zeros, d_out=N, dtype=F, workspace=ws), want)
+    with pytest.raises(q.LoraNF4Error):
+        q.w4_matvec(x, codes, scales, zeros, d_out=N, dtype=F, workspace=ws[:need - 256])
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    got = []
+    for i in range(8):
+        with torch.cuda.stream(streams[i % 2]):
+            got.append(q.w4_matvec(x, codes, scales, zeros, d_out=N, dtype=F))
+    torch.cuda.synchronize()
+    assert all(torch.equal(g, want) for g in got)
+
+
+def test_two_graphs_share_a_workspace(q):
+    T, K, N = 3, 16384, 130
+    need = q.w4_matvec_workspace_bytes(T, K, N)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    sides = []
+    for seed in (63, 64):
+        p = packed(seed, N, K, 128, False)
+        x = make(seed, T, K).cuda()
+        run = lambda p=p, x=x: q.w4_matvec(x, p[0], p[1], d_out=N, dtype=F, workspace=ws)  # noqa: E731
+        run()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = run()
+        sides.append((graph, out, run, x))
+    for i in range(4):
+        for graph, out, run, x in sides:
+            x.copy_(make(100 + i, T, K))
+            graph.replay()
+        torch.cuda.synchronize()
+        for graph, out, run, x in sides:
+            assert torch.equal(out, run())
 
 
 def test_w4_matvec_guard_bands(q):

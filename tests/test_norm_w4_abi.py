@@ -103,7 +103,7 @@ def test_packing_refusals(lib, f):
     assert f(lib, c=None) == f(lib, s=None) == f(lib, dt=E4M3) == f(lib, N=0) == f(lib, K=0) == EINVAL
     assert f(lib, g=0) == f(lib, g=16) == f(lib, g=48) == f(lib, g=256) == ESHAPE
     assert f(lib, K=100) == f(lib, K=32, g=32) == f(lib, g=128) == f(lib, K=(1 << 22) + 64) == ESHAPE
-    assert f(lib, N=1 << 31) == f(lib, N=1 << 30, K=1 << 20) == ESHAPE
+    assert f(lib, N=1 << 31) == f(lib, N=1 << 30, K=1 << 20) == f(lib, N=1 << 28, K=64) == ESHAPE
     assert f(lib, c=at(1) + 4) == f(lib, z=at(3) + 1) == EALIGN
     assert f(lib, c=at(0)) == (EALIAS)
 
@@ -118,6 +118,7 @@ def test_matvec_refusals(lib):
     assert mv(lib, g=16) == mv(lib, g=128) == mv(lib, K=200) == mv(lib, T=(1 << 21) + 1) == ESHAPE
     assert mv(lib, x=P + 8) == mv(lib, xs=at(4) + 4) == mv(lib, z=at(5) + 8) == mv(lib, y=at(3) + 2) == EALIGN
     assert mv(lib, y=P) == mv(lib, y=at(1)) == mv(lib, xs=at(3)) == EALIAS
+    assert mv(lib, T=1 << 21, N=1 << 15) == ESHAPE  # outputs of one launch
     assert mv(lib, T=0, x=None, y=None) == OK
 
 
