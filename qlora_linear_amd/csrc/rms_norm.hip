@@ -450,17 +450,29 @@ __global__ __launch_bounds__(kLoop) void rmsnorm_bwd_loop_kernel(int64_t T, int 
   }
 }
 
-// part[b][i] = sum of dy n over the rows b, b + blocks, ... of column i.
+// part[b][i] = sum of dy n over the rows b, b + blocks, ... of column i; one vector of
+// columns a thread.
 template <typename E>
 __global__ __launch_bounds__(256) void rmsnorm_dw_part_kernel(int64_t T, int d, const E* __restrict__ dy,
                                                               const E* __restrict__ h,
                                                               const float* __restrict__ rstd,
                                                               float* __restrict__ part) {
-  const int i = blockIdx.x * 256 + threadIdx.x;
-  if (i >= d) return;
-  float s = 0.f;
-  for (int64_t t = blockIdx.y; t < T; t += gridDim.y) s += to_f32(dy[t * d + i]) * (to_f32(h[t * d + i]) * rstd[t]);
-  part[static_cast<int64_t>(blockIdx.y) * d + i] = s;
+  constexpr int kN = Vec<E>::kN;
+  const int at = (blockIdx.x * 256 + threadIdx.x) * kN;
+  if (at >= d) return;
+  float s[kN];
+#pragma unroll
+  for (int j = 0; j < kN; ++j) s[j] = 0.f;
+  for (int64_t t = blockIdx.y; t < T; t += gridDim.y) {
+    const Held<E> g = load_vec(dy + t * d + at, d - at), v = load_vec(h + t * d + at, d - at);
+    const float r = rstd[t];
+#pragma unroll
+    for (int j = 0; j < kN; ++j) s[j] += elem(g, j) * (elem(v, j) * r);
+  }
+  float* const out = part + static_cast<int64_t>(blockIdx.y) * d + at;
+#pragma unroll
+  for (int j = 0; j < kN; ++j)
+    if (at + j < d) out[j] = s[j];
 }
 
 // dw[i] = sum over blocks of part[block][i]: 32 columns a workgroup, 32 threads a
@@ -567,17 +579,24 @@ hipError_t bwd(int64_t T, int d, const void* dyv, const void* dhv, const void* h
   const auto w = static_cast<const E*>(wv);
   const auto dx = static_cast<E*>(dxv), dw = static_cast<E*>(dwv);
   const auto part = static_cast<float*>(workspace);
-  // (dw's sums take a register an element: 16 elements a thread leave four waves a SIMD)
-  const RowShape sh = row_shape(T, (d + Vec<E>::kN - 1) / Vec<E>::kN, dw != nullptr ? 16 / Vec<E>::kN : 4, 32 / Vec<E>::kN);
+  // dw's sums take a register an element: 16 elements a thread leave four waves a SIMD. Rows
+  // too wide for that have dx and dw in two passes.
+  constexpr int kMostDw = 16 / Vec<E>::kN;
+  const int64_t vecs = (d + Vec<E>::kN - 1) / Vec<E>::kN;
+  RowShape sh = row_shape(T, vecs, kMostDw, kMostDw);
+  const bool both = dw != nullptr && sh.tpr != 0;
+  if (!both) sh = row_shape(T, vecs, 4, 32 / Vec<E>::kN);
   int blocks = bwd_blocks(T);
   auto go = [&](auto tpr, auto nv) {
     constexpr int kTpr = decltype(tpr)::value, kNv = decltype(nv)::value;
     constexpr int kBlock = kTpr < kBwdThreads ? kBwdThreads : kTpr, kSlots = kBlock / kTpr;
-    blocks = static_cast<int>(std::min<int64_t>((T + kSlots - 1) / kSlots, blocks));
-    if (dw != nullptr)
-      rmsnorm_bwd_kernel<E, kTpr, kNv, kBlock, true><<<dim3(blocks), kBlock, 0, stream>>>(T, d, dy, dh, h, w, rstd, dx, part);
-    else
-      rmsnorm_bwd_kernel<E, kTpr, kNv, kBlock, false><<<dim3(blocks), kBlock, 0, stream>>>(T, d, dy, dh, h, w, rstd, dx, part);
+    const int n = static_cast<int>(std::min<int64_t>((T + kSlots - 1) / kSlots, blocks));
+    if (!both) {
+      rmsnorm_bwd_kernel<E, kTpr, kNv, kBlock, false><<<dim3(n), kBlock, 0, stream>>>(T, d, dy, dh, h, w, rstd, dx, part);
+    } else if constexpr (kNv <= kMostDw) {
+      blocks = n;
+      rmsnorm_bwd_kernel<E, kTpr, kNv, kBlock, true><<<dim3(n), kBlock, 0, stream>>>(T, d, dy, dh, h, w, rstd, dx, part);
+    }
   };
   auto pick = [&](auto tpr) {
     switch (sh.nv) {
@@ -592,12 +611,10 @@ hipError_t bwd(int64_t T, int d, const void* dyv, const void* dhv, const void* h
   if (sh.tpr == 64) pick(std::integral_constant<int, 64>{});
   else if (sh.tpr == 256) pick(std::integral_constant<int, 256>{});
   else if (sh.tpr == 1024) pick(std::integral_constant<int, 1024>{});
-  else {
-    rmsnorm_bwd_loop_kernel<E><<<row_grid(T), kLoop, 0, stream>>>(T, d, dy, dh, h, w, rstd, dx);
-    if (dw != nullptr) {
-      blocks = std::min(blocks, 64);
-      rmsnorm_dw_part_kernel<E><<<dim3((d + 255) / 256, blocks), 256, 0, stream>>>(T, d, dy, h, rstd, part);
-    }
+  else rmsnorm_bwd_loop_kernel<E><<<row_grid(T), kLoop, 0, stream>>>(T, d, dy, dh, h, w, rstd, dx);
+  if (dw != nullptr && !both) {
+    blocks = std::min(blocks, 64);
+    rmsnorm_dw_part_kernel<E><<<dim3(static_cast<unsigned>((vecs + 255) / 256), blocks), 256, 0, stream>>>(T, d, dy, h, rstd, part);
   }
   if (dw != nullptr) rmsnorm_dw_kernel<E><<<dim3((d + 31) / 32), 1024, 0, stream>>>(blocks, d, part, dw);
   return hipGetLastError();
