@@ -510,22 +510,43 @@ __global__ __launch_bounds__(256) void zero_kernel(E* __restrict__ p, int64_t n)
   if (i < n) p[i] = E(0);
 }
 
-// Threads and vectors a thread of a row of `vecs` vectors. Many rows: one wave a row (no
-// barrier) up to `most` vectors a lane, then 4 waves, then 16. Few rows leave the GPU idle
-// whatever is chosen, so a row takes as many threads as have a vector: fewer loads one
-// after another on the path from the first load to the last store.
+// Threads and vectors a thread of a row of `vecs` vectors: up to two vectors a thread, from
+// one wave, 4 or 16, as long as 16 waves of two hold the row. Measured (bf16 forward with
+// residual, us): 8192 x 4096 at 256 threads of two 47, 1024 of one 49, 64 of eight 55; 1 x
+// 4096 at 256 of two 2.9, 64 of eight 5.3; 8192 x 1024 at 64 of two 11.1, 256 of one 12.9;
+// but 400 x 1024 at 256 of one 2.9, 64 of two 4.2 (few rows leave the GPU idle whatever
+// is chosen, and one vector a thread has the shorter way from its loads to its stores).
+// most: the most vectors of 1024 threads.
 constexpr int kFewRows = 512;
 struct RowShape {
   int tpr, nv;  // tpr 0: does not fit
 };
-RowShape row_shape(int64_t T, int64_t vecs, int most, int most1024) {
-  const int nv64 = static_cast<int>((vecs + 63) / 64), nv256 = static_cast<int>((vecs + 255) / 256);
-  const int nv1024 = static_cast<int>((vecs + 1023) / 1024);
-  auto up = [](int n) { return n <= 1 ? 1 : n <= 2 ? 2 : n <= 4 ? 4 : 8; };
-  if (nv64 == 1 || (T > kFewRows && nv64 <= most)) return {64, up(nv64)};
-  if (nv256 == 1 || (T > kFewRows && nv256 <= most)) return {256, up(nv256)};
-  if (nv1024 <= most1024) return {1024, up(nv1024)};
+RowShape row_shape(int64_t T, int64_t vecs, int most) {
+  if (vecs <= 64) return {64, 1};
+  if (vecs <= 128 && T > kFewRows) return {64, 2};
+  if (vecs <= 256) return {256, 1};
+  if (vecs <= 512) return {256, 2};
+  for (int nv = 1; nv <= most; nv *= 2)
+    if (vecs <= 1024 * nv) return {1024, nv};
   return {0, 0};
+}
+// go(threads, vectors) of a shape, as compile-time constants.
+template <int MOST, class Go>
+void with_shape(const RowShape& sh, Go&& go) {
+  using std::integral_constant;
+  const integral_constant<int, 64> t64;
+  const integral_constant<int, 256> t256;
+  const integral_constant<int, 1024> t1024;
+  const integral_constant<int, 1> one;
+  const integral_constant<int, 2> two;
+  if (sh.tpr == 64) sh.nv == 1 ? go(t64, one) : go(t64, two);
+  else if (sh.tpr == 256) sh.nv == 1 ? go(t256, one) : go(t256, two);
+  else if (sh.nv == 1) go(t1024, one);
+  else if (sh.nv == 2) go(t1024, two);
+  else if constexpr (MOST >= 4) {
+    if (sh.nv == 4) go(t1024, integral_constant<int, 4>{});
+    else if constexpr (MOST >= 8) go(t1024, integral_constant<int, 8>{});
+  }
 }
 
 template <typename E, int OUT>
@@ -533,28 +554,16 @@ hipError_t fwd(int64_t T, int d, float eps, const void* xv, const void* rv, cons
                float* q_scale, float* rstd, hipStream_t stream) {
   const auto x = static_cast<const E*>(xv), res = static_cast<const E*>(rv), w = static_cast<const E*>(wv);
   const auto h = static_cast<E*>(hv);
-  const RowShape sh = row_shape(T, (d + Vec<E>::kN - 1) / Vec<E>::kN, 4, 32 / Vec<E>::kN);
-  auto go = [&](auto tpr, auto nv) {
-    constexpr int kTpr = decltype(tpr)::value, kNv = decltype(nv)::value, kRows = kTpr < 256 ? 256 / kTpr : 1;
-    rmsnorm_fwd_kernel<E, OUT, kTpr, kNv><<<row_grid((T + kRows - 1) / kRows), kTpr * kRows, 0, stream>>>(
-        T, d, eps, x, res, w, h, y, q_scale, rstd);
-  };
-  auto pick = [&](auto tpr) {
-    switch (sh.nv) {
-      case 1: go(tpr, std::integral_constant<int, 1>{}); break;
-      case 2: go(tpr, std::integral_constant<int, 2>{}); break;
-      case 4: go(tpr, std::integral_constant<int, 4>{}); break;
-      default:
-        if constexpr (decltype(tpr)::value == 1024 && sizeof(E) == 4) go(tpr, std::integral_constant<int, 8>{});
-        break;
-    }
-  };
-  if (sh.tpr == 64) pick(std::integral_constant<int, 64>{});
-  else if (sh.tpr == 256) pick(std::integral_constant<int, 256>{});
-  else if (sh.tpr == 1024) pick(std::integral_constant<int, 1024>{});
+  constexpr int kMost = 32 / Vec<E>::kN;
+  const RowShape sh = row_shape(T, (d + Vec<E>::kN - 1) / Vec<E>::kN, kMost);
+  if (sh.tpr == 0)
+    rmsnorm_fwd_loop_kernel<E, OUT><<<row_grid(T), kLoop, 0, stream>>>(T, d, eps, x, res, w, h, y, q_scale, rstd);
   else
-    rmsnorm_fwd_loop_kernel<E, OUT><<<row_grid(T), kLoop, 0, stream>>>(T, d, eps, x, res, w, h, y,
-                                                                                          q_scale, rstd);
+    with_shape<kMost>(sh, [&](auto tpr, auto nv) {
+      constexpr int kTpr = decltype(tpr)::value, kNv = decltype(nv)::value, kRows = kTpr < 256 ? 256 / kTpr : 1;
+      rmsnorm_fwd_kernel<E, OUT, kTpr, kNv><<<row_grid((T + kRows - 1) / kRows), kTpr * kRows, 0, stream>>>(
+          T, d, eps, x, res, w, h, y, q_scale, rstd);
+    });
   return hipGetLastError();
 }
 
@@ -580,38 +589,27 @@ hipError_t bwd(int64_t T, int d, const void* dyv, const void* dhv, const void* h
   const auto dx = static_cast<E*>(dxv), dw = static_cast<E*>(dwv);
   const auto part = static_cast<float*>(workspace);
   // dw's sums take a register an element: 16 elements a thread leave four waves a SIMD. Rows
-  // too wide for that have dx and dw in two passes.
-  constexpr int kMostDw = 16 / Vec<E>::kN;
+  // too wide for that have dx and dw in two passes (with 32 the 1024-thread workgroup
+  // spills: 1 x 27952 bf16 24 us in one pass, 16 in two).
+  constexpr int kMost = 32 / Vec<E>::kN, kMostDw = 16 / Vec<E>::kN;
   const int64_t vecs = (d + Vec<E>::kN - 1) / Vec<E>::kN;
-  RowShape sh = row_shape(T, vecs, kMostDw, kMostDw);
-  const bool both = dw != nullptr && sh.tpr != 0;
-  if (!both) sh = row_shape(T, vecs, 4, 32 / Vec<E>::kN);
+  const RowShape sh = row_shape(T, vecs, kMost);
+  const bool both = dw != nullptr && sh.tpr != 0 && sh.nv <= kMostDw;
   int blocks = bwd_blocks(T);
-  auto go = [&](auto tpr, auto nv) {
-    constexpr int kTpr = decltype(tpr)::value, kNv = decltype(nv)::value;
-    constexpr int kBlock = kTpr < kBwdThreads ? kBwdThreads : kTpr, kSlots = kBlock / kTpr;
-    const int n = static_cast<int>(std::min<int64_t>((T + kSlots - 1) / kSlots, blocks));
-    if (!both) {
-      rmsnorm_bwd_kernel<E, kTpr, kNv, kBlock, false><<<dim3(n), kBlock, 0, stream>>>(T, d, dy, dh, h, w, rstd, dx, part);
-    } else if constexpr (kNv <= kMostDw) {
-      blocks = n;
-      rmsnorm_bwd_kernel<E, kTpr, kNv, kBlock, true><<<dim3(n), kBlock, 0, stream>>>(T, d, dy, dh, h, w, rstd, dx, part);
-    }
-  };
-  auto pick = [&](auto tpr) {
-    switch (sh.nv) {
-      case 1: go(tpr, std::integral_constant<int, 1>{}); break;
-      case 2: go(tpr, std::integral_constant<int, 2>{}); break;
-      case 4: go(tpr, std::integral_constant<int, 4>{}); break;
-      default:
-        if constexpr (decltype(tpr)::value == 1024 && sizeof(E) == 4) go(tpr, std::integral_constant<int, 8>{});
-        break;
-    }
-  };
-  if (sh.tpr == 64) pick(std::integral_constant<int, 64>{});
-  else if (sh.tpr == 256) pick(std::integral_constant<int, 256>{});
-  else if (sh.tpr == 1024) pick(std::integral_constant<int, 1024>{});
-  else rmsnorm_bwd_loop_kernel<E><<<row_grid(T), kLoop, 0, stream>>>(T, d, dy, dh, h, w, rstd, dx);
+  if (sh.tpr == 0)
+    rmsnorm_bwd_loop_kernel<E><<<row_grid(T), kLoop, 0, stream>>>(T, d, dy, dh, h, w, rstd, dx);
+  else
+    with_shape<kMost>(sh, [&](auto tpr, auto nv) {
+      constexpr int kTpr = decltype(tpr)::value, kNv = decltype(nv)::value;
+      constexpr int kBlock = kTpr < kBwdThreads ? kBwdThreads : kTpr, kSlots = kBlock / kTpr;
+      const int n = static_cast<int>(std::min<int64_t>((T + kSlots - 1) / kSlots, blocks));
+      if (!both) {
+        rmsnorm_bwd_kernel<E, kTpr, kNv, kBlock, false><<<dim3(n), kBlock, 0, stream>>>(T, d, dy, dh, h, w, rstd, dx, part);
+      } else if constexpr (kNv <= kMostDw) {
+        blocks = n;
+        rmsnorm_bwd_kernel<E, kTpr, kNv, kBlock, true><<<dim3(n), kBlock, 0, stream>>>(T, d, dy, dh, h, w, rstd, dx, part);
+      }
+    });
   if (dw != nullptr && !both) {
     blocks = std::min(blocks, 64);
     rmsnorm_dw_part_kernel<E><<<dim3(static_cast<unsigned>((vecs + 255) / 256), blocks), 256, 0, stream>>>(T, d, dy, h, rstd, part);

@@ -43,7 +43,7 @@ def add_rounded(x, res):
 
 # ---- norm ---------------------------------------------------------------------------
 NORM = [(1, 1), (3, 7), (1, 64), (5, 100), (2, 1001), (9, 2048), (33, 4096), (2, 5003), (4, 5120), (3, 8192),
-        (2, 11008), (1, 28672), (2, 32768), (1, 40000), (2, 33333), (700, 96)]
+        (2, 11008), (1, 28672), (2, 32768), (1, 40000), (2, 33333), (700, 96), (600, 1000), (530, 333)]
 
 
 @pytest.mark.parametrize("dtype", [BF, F], ids=["bf16", "f32"])
