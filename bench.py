@@ -20,7 +20,8 @@ weight-streaming kernels, bound by reading the packed weight), back to back and
 cold (after a 1 GiB read), and `small_tokens_headline_projection` the headline
 projection at a few tokens; `medium_tokens` does the same at a few hundred
 tokens (tiled kernels on a grid of 128 x 128 tiles); `merge` times lora_nf4_merge of that
-projection (the 16-bit export, also HBM-bound); `rank_r_gradients` times the backward's
+projection (the 16-bit export, also HBM-bound); `served_projection` the merged weight packed to
+4 bits and multiplied with the norm's 8-bit rows, and the norm forward and backward; `rank_r_gradients` times the backward's
 rank-r step alone (lora_nf4_grad_ab, bound by reading x and dY); `train_step` times the AdamW step of A and B and the
 absmax double quantization; `multi_projection` times Llama-3-8B q/k/v (r = 64, one x) as one
 lora_nf4_fwd_multi + lora_nf4_bwd_multi against separate calls. With --fuse, projections that read the same
@@ -479,6 +480,66 @@ def merge_run(lib, q, torch, d, w, sp, reps=20):
     return {"projection": f"{p.name} {K}->{N}", "r": r, "us": round(us, 2), "bytes": nbytes,
             "bound": "hbm", "achieved": round(nbytes / us / 1e3, 1), "peak": PEAK_HBM_GBS, "unit": "GB/s",
             "frac": round(nbytes / us / 1e3 / PEAK_HBM_GBS, 4)}
+
+
+def serve_run(lib, q, torch, d, w, sp, rows=(1, 16), group=128, reps=50):
+    """The merged projection as it is served, and the norm in front of it: the weight of
+    lora_nf4_merge packed to 4 bits (w4_quantize), then for a few rows rmsnorm_fwd_quant (E4M3,
+    residual added) and w4_matvec of its rows, HIP events around `reps` back-to-back C-ABI calls
+    each; bytes of the product = packed weight + x + y. And the training side at the workload's
+    token count: rmsnorm_fwd with the residual and rmsnorm_bwd with the weight's gradient, both
+    8 bytes a bf16 element (x, residual, h, y; dy, dh, h, dx)."""
+    p = d["p"]
+    K, N = p.d_in, p.d_out
+    bf, f32 = torch.bfloat16, torch.float32
+    codes, scales, _ = q.w4_quantize(q.lora_nf4_merge(d["codes"], d["absmax"], d["A"], d["B"], w.alpha), group)
+    packed = codes.numel() + scales.numel() * 2
+    weight = torch.ones(K, dtype=bf, device="cuda")
+
+    def timed(name, call, nbytes):
+        def checked():
+            st = call()
+            if st != 0:
+                raise q.LoraNF4Error(name, st)
+
+        for _ in range(5):
+            checked()
+        e0, e1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        e0.record()
+        for _ in range(reps):
+            checked()
+        e1.record()
+        torch.cuda.synchronize()
+        us = e0.elapsed_time(e1) * 1000.0 / reps
+        return {"us": round(us, 2), "achieved": round(nbytes / us / 1e3, 1), "peak": PEAK_HBM_GBS, "unit": "GB/s",
+                "frac": round(nbytes / us / 1e3 / PEAK_HBM_GBS, 4)}
+
+    out = {"projection": f"{p.name} {K}->{N}", "group": group, "bound": "hbm", "packed_bytes": packed, "rows": {}}
+    for T in rows:
+        x, res = (torch.randn(T, K, device="cuda").to(bf) for _ in range(2))
+        h, y = torch.empty_like(x), torch.empty((T, N), dtype=bf, device="cuda")
+        lv, sc = torch.empty((T, K), dtype=torch.uint8, device="cuda"), torch.empty(T, dtype=f32, device="cuda")
+        need = q.w4_matvec_workspace_bytes(T, K, N)
+        ws = torch.empty(max(need, 256), dtype=torch.uint8, device="cuda")
+        out["rows"][str(T)] = {
+            "norm_quant": timed("rmsnorm_fwd_quant", lambda: lib.rmsnorm_fwd_quant(
+                T, K, 1, 1e-5, x.data_ptr(), res.data_ptr(), weight.data_ptr(), h.data_ptr(), q.LN_E4M3,
+                lv.data_ptr(), sc.data_ptr(), sp), T * K * 7 + K * 2),
+            "product": timed("w4_matvec", lambda: lib.w4_matvec(
+                T, K, N, group, q.LN_E4M3, lv.data_ptr(), sc.data_ptr(), codes.data_ptr(), scales.data_ptr(), None, 1,
+                y.data_ptr(), ws.data_ptr(), ws.numel(), sp), packed + T * K + T * N * 2)}
+    T = w.tokens
+    a = [torch.randn(T, K, device="cuda").to(bf) for _ in range(2)] + [torch.empty((T, K), dtype=bf, device="cuda")
+                                                                       for _ in range(2)]
+    rstd, dw = torch.empty(T, dtype=f32, device="cuda"), torch.empty(K, dtype=bf, device="cuda")
+    ws = torch.empty(max(q.rmsnorm_bwd_workspace_bytes(T, K), 256), dtype=torch.uint8, device="cuda")
+    x, res, h, y = (t.data_ptr() for t in a)
+    out["norm_fwd"] = timed("rmsnorm_fwd", lambda: lib.rmsnorm_fwd(
+        T, K, 1, 1e-5, x, res, weight.data_ptr(), h, y, rstd.data_ptr(), sp), T * K * 8)
+    out["norm_bwd"] = timed("rmsnorm_bwd", lambda: lib.rmsnorm_bwd(
+        T, K, 1, x, res, h, weight.data_ptr(), rstd.data_ptr(), y, dw.data_ptr(), ws.data_ptr(), ws.numel(), sp),
+        T * K * 8)
+    return out
 
 
 def rank_r_run(lib, q, torch, d, w, sp, reps=50):
@@ -1212,6 +1273,7 @@ def main():
     if args.medium_tokens > 0:
         out["medium_tokens"] = medium_token_run(lib, q, torch, run.projs[run.units[bu][0]], w, args.medium_tokens, sp)
     out["merge"] = merge_run(lib, q, torch, run.projs[run.units[bu][0]], w, sp)
+    out["served_projection"] = serve_run(lib, q, torch, run.projs[run.units[bu][0]], w, sp)
     out["rank_r_gradients"] = rank_r_run(lib, q, torch, run.projs[run.units[bu][0]], w, sp)
     out["train_step"] = train_step_run(lib, q, torch, run.projs[run.units[bu][0]], w, sp)
     progress("small / medium tokens, merge, training step done")
