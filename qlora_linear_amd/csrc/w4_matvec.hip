@@ -131,20 +131,42 @@ __device__ __forceinline__ void spread(uint32_t v, uint32_t (&o)[GP]) {
   }
 }
 
-// TB: 16-row blocks of x; R: tiles a workgroup; W: waves; D: chunks in flight; G: group.
-template <int XT, int TB, int R, int W, int D, int G, bool ZERO>
-__global__ __launch_bounds__(W * 64) void w4_matvec_kernel(int64_t T, int K, const uint8_t* __restrict__ x,
+// Scales and zero points of a chunk's groups as floats, from the lane's raw ones.
+template <int GP, bool ZERO>
+__device__ __forceinline__ void group_factors(uint32_t scale, uint32_t zero, float (&s)[GP], float (&z)[GP]) {
+  uint32_t v[GP];
+  spread<GP>(scale | zero << 16, v);
+#pragma unroll
+  for (int j = 0; j < GP; ++j) {
+    s[j] = __uint_as_float(v[j] << 16);
+    z[j] = ZERO ? static_cast<float>(v[j] >> 16) : 0.f;
+  }
+}
+
+// tot += s (acc + z xs) of a 16 x 16 block, xs holding -sum x (without zero points
+// -8 sum x, and z is not used).
+template <bool ZERO, typename Acc>
+__device__ __forceinline__ void add_group(const Acc& acc, const Acc& xs, float s, float z, float (&tot)[4]) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float u = ZERO ? static_cast<float>(acc[e]) + z * static_cast<float>(xs[e]) : static_cast<float>(acc[e] + xs[e]);
+    tot[e] += s * u;
+  }
+}
+
+// Up to 16 rows of x. R: tiles a workgroup; W: waves; D: chunks in flight; G: group.
+template <int XT, int R, int W, int D, int G, bool ZERO>
+__global__ __launch_bounds__(W * 64) void w4_matvec_kernel(int T, int K, const uint8_t* __restrict__ x,
                                                            const float* __restrict__ x_scale, const W4Table tab,
-                                                           int t_blocks, bool y_bf16) {
+                                                           bool y_bf16) {
   using X = Rows<XT>;
   using Op = typename X::Op;
   using Acc = typename X::Acc;
   constexpr int GP = 128 / G;
-  __shared__ float red[W][R * TB * 4][64];
+  __shared__ float red[W][R * 4][64];
   const int lane = threadIdx.x & 63, l16 = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t t0 = static_cast<int64_t>(blockIdx.x % t_blocks) * (16 * TB);
-  int group = blockIdx.x / t_blocks, p = 0;
+  int group = blockIdx.x, p = 0;
   while (group >= tab.group_end[p]) ++p;
   if (p > 0) group -= tab.group_end[p - 1];
   const int N = tab.N[p], nt = (N + 15) / 16, kt = (K + 127) / 128, kg = K / G;
@@ -158,12 +180,9 @@ __global__ __launch_bounds__(W * 64) void w4_matvec_kernel(int64_t T, int K, con
     scale_rs[r] = make_rsrc(tab.scales[p] + tile * kg * 16, kg * 32);
     if constexpr (ZERO) zero_rs[r] = make_rsrc(tab.zeros[p] + tile * kg * 16, kg * 16);
   }
-  // the block's rows of x; a row past T reads the last one (its sums are not stored)
-  const int rows = static_cast<int>(min(T - t0, static_cast<int64_t>(16 * TB)));
-  const auto x_rs = make_rsrc(x + t0 * K * X::kBytes, static_cast<uint32_t>(rows) * K * X::kBytes);
-  uint32_t x_at[TB];
-#pragma unroll
-  for (int b = 0; b < TB; ++b) x_at[b] = (static_cast<uint32_t>(min(16 * b + l16, rows - 1)) * K + 8 * g) * X::kBytes;
+  // (a row past T reads the last one; its sums are not stored)
+  const auto x_rs = make_rsrc(x, static_cast<uint32_t>(T) * K * X::kBytes);
+  const uint32_t x_at = (static_cast<uint32_t>(min(l16, T - 1)) * K + 8 * g) * X::kBytes;
   // the lane's group of a chunk; where only the first half exists, a group of that
   const uint32_t group_at = (GP == 1 ? 0 : GP == 2 ? g >> 1 : g) * 16 + l16;
   const uint32_t group_at_half = (GP == 4 ? g & 1 : 0) * 16 + l16;
@@ -171,7 +190,7 @@ __global__ __launch_bounds__(W * 64) void w4_matvec_kernel(int64_t T, int K, con
   struct Chunk {
     uint4 codes[R];
     uint32_t scale[R], zero[R];
-    Op x[TB][4];
+    Op x[4];
   };
   Chunk ring[D];
   const int nw = kt > wave ? (kt - wave + W - 1) / W : 0;  // chunks of this wave
@@ -188,96 +207,62 @@ __global__ __launch_bounds__(W * 64) void w4_matvec_kernel(int64_t T, int K, con
     // (in place of a half that does not exist the first one is read; its scales become 0)
     const uint32_t x0 = at * 128 * X::kBytes, x1 = x0 + (half ? 0 : 64 * X::kBytes);
 #pragma unroll
-    for (int b = 0; b < TB; ++b)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) c.x[b][q] = X::load(x_rs, x_at[b] + 32 * (q & 1) * X::kBytes, q < 2 ? x0 : x1);
+    for (int q = 0; q < 4; ++q) c.x[q] = X::load(x_rs, x_at + 32 * (q & 1) * X::kBytes, q < 2 ? x0 : x1);
   };
 
-  float tot[R][TB][4];
+  float tot[R][4];
 #pragma unroll
   for (int r = 0; r < R; ++r)
 #pragma unroll
-    for (int b = 0; b < TB; ++b)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) tot[r][b][j] = 0.f;
+    for (int e = 0; e < 4; ++e) tot[r][e] = 0.f;
   const typename X::Wide minus = X::minus(!ZERO);
-  auto step = [&](int i, Chunk& c) {
+  auto step = [&](int i, const Chunk& c) {
     const bool absent = GP > 1 && (wave + W * i) * 128 + 64 == K && g >= 2;  // the lane's group
     float s[R][GP], z[R][GP];
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      uint32_t v[GP];
-      spread<GP>(absent ? 0u : c.scale[r] | (ZERO ? c.zero[r] << 16 : 0u), v);
-#pragma unroll
-      for (int j = 0; j < GP; ++j) {
-        s[r][j] = __uint_as_float(v[j] << 16);
-        if constexpr (ZERO) z[r][j] = static_cast<float>(v[j] >> 16);
-      }
-    }
-    Acc acc[R][TB], xs[TB];
+    for (int r = 0; r < R; ++r) group_factors<GP, ZERO>(absent ? 0u : c.scale[r], ZERO ? c.zero[r] : 0u, s[r], z[r]);
+    Acc acc[R], xs;
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       const bool first = q * 32 % G == 0;
-      typename X::Wide xq[TB];
-#pragma unroll
-      for (int b = 0; b < TB; ++b) {
-        xq[b] = X::widen(c.x[b][q]);
-        xs[b] = X::mma(xq[b], minus, first ? Acc{} : xs[b]);
-      }
+      const typename X::Wide xq = X::widen(c.x[q]);
+      xs = X::mma(xq, minus, first ? Acc{} : xs);
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         const uint32_t words[4] = {c.codes[r].x, c.codes[r].y, c.codes[r].z, c.codes[r].w};
-        const typename X::Wide w = X::codes(words[q]);
-#pragma unroll
-        for (int b = 0; b < TB; ++b) acc[r][b] = X::mma(xq[b], w, first ? Acc{} : acc[r][b]);
+        acc[r] = X::mma(xq, X::codes(words[q]), first ? Acc{} : acc[r]);
       }
       if ((q + 1) * 32 % G == 0) {
-        const int j = q * 32 / G;
 #pragma unroll
-        for (int r = 0; r < R; ++r)
-#pragma unroll
-          for (int b = 0; b < TB; ++b)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              float u;
-              if constexpr (ZERO)
-                u = static_cast<float>(acc[r][b][e]) + z[r][j] * static_cast<float>(xs[b][e]);
-              else
-                u = static_cast<float>(acc[r][b][e] + xs[b][e]);
-              tot[r][b][e] += s[r][j] * u;
-            }
+        for (int r = 0; r < R; ++r) add_group<ZERO>(acc[r], xs, s[r][q * 32 / G], z[r][q * 32 / G], tot[r]);
       }
     }
   };
-  if (nw > 0) {
 #pragma unroll
-    for (int d = 0; d < D; ++d)
-      if (d < nw) load(d, ring[d]);
-    for (int i = 0; i < nw; i += D) {
+  for (int d = 0; d < D; ++d)
+    if (d < nw) load(d, ring[d]);
+  for (int i = 0; i < nw; i += D) {
 #pragma unroll
-      for (int d = 0; d < D; ++d) {
-        if (i + d < nw) step(i + d, ring[d]);
-        if (i + d + D < nw) load(i + d + D, ring[d]);
-      }
+    for (int d = 0; d < D; ++d) {
+      if (i + d < nw) step(i + d, ring[d]);
+      if (i + d + D < nw) load(i + d + D, ring[d]);
     }
   }
 #pragma unroll
   for (int r = 0; r < R; ++r)
 #pragma unroll
-    for (int b = 0; b < TB; ++b)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) red[wave][(r * TB + b) * 4 + e][lane] = tot[r][b][e];
+    for (int e = 0; e < 4; ++e) red[wave][r * 4 + e][lane] = tot[r][e];
   __syncthreads();
-  for (int o = threadIdx.x; o < R * TB * 256; o += W * 64) {
+  for (int o = threadIdx.x; o < R * 256; o += W * 64) {
     const int e = o >> 6, ln = o & 63;
-    const int64_t t = t0 + e / 4 % TB * 16 + 4 * (ln >> 4) + e % 4;
-    const int n = (group * R + e / (4 * TB)) * 16 + (ln & 15);
+    const int t = 4 * (ln >> 4) + e % 4;
+    const int n = (group * R + e / 4) * 16 + (ln & 15);
     if (t >= T || n >= N) continue;
     float v = 0.f;
 #pragma unroll
     for (int w = 0; w < W; ++w) v += red[w][e][ln];
     if (x_scale != nullptr) v *= x_scale[t];
-    const int64_t at = t * N + n;
+    const int64_t at = static_cast<int64_t>(t) * N + n;
     if (y_bf16) static_cast<uint16_t*>(tab.y[p])[at] = to_bf16(v);
     else static_cast<float*>(tab.y[p])[at] = v;
   }
@@ -392,15 +377,7 @@ __global__ __launch_bounds__(RW * KW * 64) void w4_matvec_shared_kernel(int64_t 
     const unsigned char* const chunk = stage + kw * kChunk;
     float s[R][GP], z[R][GP];
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      uint32_t v[GP];
-      spread<GP>(absent ? 0u : c.scale[r] | (ZERO ? c.zero[r] << 16 : 0u), v);
-#pragma unroll
-      for (int j = 0; j < GP; ++j) {
-        s[r][j] = __uint_as_float(v[j] << 16);
-        if constexpr (ZERO) z[r][j] = static_cast<float>(v[j] >> 16);
-      }
-    }
+    for (int r = 0; r < R; ++r) group_factors<GP, ZERO>(absent ? 0u : c.scale[r], ZERO ? c.zero[r] : 0u, s[r], z[r]);
     Acc acc[R][TB], xs[TB];
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
@@ -423,16 +400,7 @@ __global__ __launch_bounds__(RW * KW * 64) void w4_matvec_shared_kernel(int64_t 
 #pragma unroll
         for (int r = 0; r < R; ++r)
 #pragma unroll
-          for (int b = 0; b < TB; ++b)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              float u;
-              if constexpr (ZERO)
-                u = static_cast<float>(acc[r][b][e]) + z[r][j] * static_cast<float>(xs[b][e]);
-              else
-                u = static_cast<float>(acc[r][b][e] + xs[b][e]);
-              tot[r][b][e] += s[r][j] * u;
-            }
+          for (int b = 0; b < TB; ++b) add_group<ZERO>(acc[r][b], xs[b], s[r][j], z[r][j], tot[r][b]);
       }
     }
   };
@@ -559,29 +527,9 @@ struct Call {
   hipStream_t stream;
 };
 
-// The launch for the call's group size and zero points: the kernel with K-split waves
-// (SHARED = 0: <XT, TB, R, W, D>) or the one with x in LDS (<XT, TB, R, RW, KW>).
-template <int XT, int TB, int R, int A, int B, int SHARED>
-hipError_t run(Call c) {
-  constexpr int kTiles = SHARED > 0 ? R * A : R;
-  int groups = 0;
-  for (int p = 0; p < c.tab.n; ++p) {
-    groups += ((c.tab.N[p] + 15) / 16 + kTiles - 1) / kTiles;
-    c.tab.group_end[p] = groups;
-  }
-  const int t_blocks = static_cast<int>((c.T + 16 * TB - 1) / (16 * TB));
-  const dim3 grid(static_cast<unsigned>(groups) * static_cast<unsigned>(t_blocks) * static_cast<unsigned>(c.splits));
-  const auto x = static_cast<const uint8_t*>(c.x);
-  auto go = [&](auto g, auto zero) {
-    constexpr int kG = decltype(g)::value;
-    constexpr bool kZero = decltype(zero)::value;
-    if constexpr (SHARED > 0)
-      w4_matvec_shared_kernel<XT, TB, R, A, B, 3, kG, kZero>
-          <<<grid, A * B * 64, 0, c.stream>>>(c.T, c.K, x, c.x_scale, c.tab, t_blocks, c.y_bf16, c.splits, c.part);
-    else
-      w4_matvec_kernel<XT, TB, R, A, B, kG, kZero>
-          <<<grid, A * 64, 0, c.stream>>>(c.T, c.K, x, c.x_scale, c.tab, t_blocks, c.y_bf16);
-  };
+// The launch for the call's group size and zero points.
+template <class Go>
+void with_group(const Call& c, Go&& go) {
   auto with = [&](auto zero) {
     if (c.group == 32) go(std::integral_constant<int, 32>{}, zero);
     else if (c.group == 64) go(std::integral_constant<int, 64>{}, zero);
@@ -589,6 +537,43 @@ hipError_t run(Call c) {
   };
   if (c.tab.zeros[0] != nullptr) with(std::true_type{});
   else with(std::false_type{});
+}
+
+// Workgroups along the rows of all weights, `tiles` tiles each.
+int set_groups(W4Table& tab, int tiles) {
+  int groups = 0;
+  for (int p = 0; p < tab.n; ++p) {
+    groups += ((tab.N[p] + 15) / 16 + tiles - 1) / tiles;
+    tab.group_end[p] = groups;
+  }
+  return groups;
+}
+
+template <int XT, int R, int W, int D>
+hipError_t run(Call c) {
+  const dim3 grid(static_cast<unsigned>(set_groups(c.tab, R)));
+  with_group(c, [&](auto g, auto zero) {
+    constexpr int kG = decltype(g)::value;
+    constexpr bool kZero = decltype(zero)::value;
+    // 16 waves of two tiles have 128 registers each: bf16 rows with four groups a chunk and
+    // zero points would spill at two chunks in flight (4096 -> 6144 at 4 rows 9.7 us, with one 5.5)
+    constexpr int kD = XT == kRowBf16 && kG == 32 && kZero && R * W > 16 ? 1 : D;
+    w4_matvec_kernel<XT, R, W, kD, kG, kZero><<<grid, W * 64, 0, c.stream>>>(
+        static_cast<int>(c.T), c.K, static_cast<const uint8_t*>(c.x), c.x_scale, c.tab, c.y_bf16);
+  });
+  return hipGetLastError();
+}
+
+template <int XT, int TB, int R, int RW, int KW>
+hipError_t run_shared(Call c) {
+  const int t_blocks = static_cast<int>((c.T + 16 * TB - 1) / (16 * TB));
+  const dim3 grid(static_cast<unsigned>(set_groups(c.tab, R * RW)) * static_cast<unsigned>(t_blocks) *
+                  static_cast<unsigned>(c.splits));
+  with_group(c, [&](auto g, auto zero) {
+    w4_matvec_shared_kernel<XT, TB, R, RW, KW, 3, decltype(g)::value, decltype(zero)::value>
+        <<<grid, RW * KW * 64, 0, c.stream>>>(c.T, c.K, static_cast<const uint8_t*>(c.x), c.x_scale, c.tab, t_blocks,
+                                              c.y_bf16, c.splits, c.part);
+  });
   if (c.splits > 1) {
     int64_t all = 0;
     for (int p = 0; p < c.tab.n; ++p) all += c.tab.N[p];
@@ -646,13 +631,13 @@ Plan plan(int64_t T, int64_t K, int n, const int* N) {
 template <int XT>
 hipError_t pick(Kind kind, const Call& c) {
   switch (kind) {
-    case kOneTile: return run<XT, 1, 1, 16, 2, 0>(c);
-    case kTwoTiles: return run<XT, 1, 2, 16, 2, 0>(c);
-    case kFourTiles: return run<XT, 1, 4, 8, 1, 0>(c);
-    case kDeep: return run<XT, 1, 1, 4, 4, 1>(c);
-    case kWide32: return run<XT, 2, 2, 4, 2, 1>(c);
-    case kWide64: return run<XT, 4, 2, 4, 2, 1>(c);
-    case kNarrow: return run<XT, 2, 1, 4, 2, 1>(c);
+    case kOneTile: return run<XT, 1, 16, 2>(c);
+    case kTwoTiles: return run<XT, 2, 16, 2>(c);
+    case kFourTiles: return run<XT, 4, 8, 1>(c);
+    case kDeep: return run_shared<XT, 1, 1, 4, 4>(c);
+    case kWide32: return run_shared<XT, 2, 2, 4, 2>(c);
+    case kWide64: return run_shared<XT, 4, 2, 4, 2>(c);
+    case kNarrow: return run_shared<XT, 2, 1, 4, 2>(c);
   }
   return hipErrorInvalidValue;
 }
