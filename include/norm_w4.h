@@ -42,8 +42,8 @@ typedef enum { LN_E4M3 = 2, LN_I8 = 3 } ln_qtype;
  *   x, residual, h, y   [T, d]; residual and h both given or both NULL
  *   w         [d]
  *   rstd      float32 [T] (output; may be NULL); rmsnorm_bwd reads it
- * T >= 0, 1 <= d <= LN_NORM_MAX_D. Rows of any width; a d that is not a multiple of
- * 16 bytes runs element by element.
+ * T >= 0, 1 <= d <= LN_NORM_MAX_D, any width (fastest where a row is a multiple of 16
+ * bytes, so that every row starts aligned). A row of NaN or infinities affects itself only.
  */
 int rmsnorm_fwd(int64_t T, int64_t d, int dtype, float eps, const void* x, const void* residual,
                 const void* w, void* h, void* y, float* rstd, void* stream);
@@ -97,8 +97,8 @@ size_t rmsnorm_bwd_workspace_bytes(int64_t T, int64_t d);
 
 /*
  * w4_quantize — packs w [d_out, d_in] (LN_F32 or LN_BF16), round to nearest-even:
- *   zeros NULL: s = bf16(f32(max|w| / 7)),  c = clamp(rint(f32(w / s)), -8, 7) + 8
- *   zeros:      lo = min(w, 0), hi = max(w, 0) over the group, s = bf16(f32(f32(hi - lo) / 15)),
+ *   zeros NULL: s = bf16(f32(max|w| f32(1/7))),  c = clamp(rint(f32(w / s)), -8, 7) + 8
+ *   zeros:      lo = min(w, 0), hi = max(w, 0) over the group, s = bf16(f32(f32(hi - lo) f32(1/15))),
  *               z = clamp(rint(f32(-lo / s)), 0, 15),  c = clamp(rint(f32(w / s)) + z, 0, 15)
  * A group with s = 0 has c = z (8, or 0 with zero points).
  */

@@ -57,7 +57,7 @@ __device__ __forceinline__ void group_extrema(int group, float& lo, float& hi) {
 
 // One 256-thread workgroup per tile. Thread t: row t >> 4, columns 8 (t & 15) .. + 7,
 // so a group is G / 8 consecutive lanes. Bound by its arithmetic rather than by HBM
-// (about 14 instructions an element): one division a thread, the codes put together as
+// (about 14 instructions an element): no division as a rule, the codes put together as
 // floats (sums of multiples of powers of 16 below 2^16 are exact), two conversions a word.
 template <typename In>
 __global__ __launch_bounds__(kThreads) void w4_quantize_kernel(const In* __restrict__ w, int64_t N, int64_t K,
@@ -80,7 +80,7 @@ __global__ __launch_bounds__(kThreads) void w4_quantize_kernel(const In* __restr
   }
   group_extrema(group, lo, hi);
   const bool asym = zeros != nullptr;
-  const uint16_t sb = to_bf16(asym ? __fdiv_rn(__fsub_rn(hi, lo), 15.f) : __fdiv_rn(fmaxf(-lo, hi), 7.f));
+  const uint16_t sb = to_bf16(asym ? (hi - lo) * (1.f / 15.f) : fmaxf(-lo, hi) * (1.f / 7.f));
   const float s = bf16_to_f32(sb);
   const float inv = __builtin_amdgcn_rcpf(s);
   float z = 8.f;
