@@ -8,15 +8,16 @@
 // sums meet in LDS. In a chunk
 //   * a lane's 16 bytes of codes are four matrix-instruction operands (32 columns each)
 //     in place: a wave reads 1024 consecutive bytes per tile, D chunks ahead;
-//   * codes become operands in registers: bytes for int8 rows (3 instructions per eight
-//     codes), and for the others bf16 by the E4M3 conversion with scale 2^9, as a byte c of
-//     0 .. 15 is c 2^-9 in E4M3, whose subnormals and first binade are equidistant (7).
-//     E4M3 rows widen to bf16 (exactly) as well: the E4M3 matrix instruction would take the
-//     nibbles as they are, but its sums lose bits (single products of 32 columns 5e-6 to
-//     1.4e-5 off, bf16 ones below 1e-8), as do f16 products with subnormal codes;
-//   * the matrix instruction multiplies codes, not weights: the group's scale and zero
-//     point are applied to its 16 x 16 sums. The zero point needs sum x over the group,
-//     one more instruction with a constant operand, shared by the R tiles;
+//   * codes become operands in registers. bf16 and E4M3 rows: bf16 by the E4M3 conversion
+//     with scale 2^9, as a byte c of 0 .. 15 is c 2^-9 in E4M3, whose subnormals and first
+//     binade are equidistant (7 instructions per eight codes). E4M3 rows widen to bf16
+//     (exactly) as well: the E4M3 matrix instruction would take the nibbles as they are, but
+//     its sums lose bits (single products of 32 columns 5e-6 to 1.4e-5 off, bf16 ones below
+//     1e-8), as do f16 products with subnormal codes. int8 rows: bytes c - z (5 and 7);
+//   * the matrix instruction multiplies codes, not weights: the group's scale, and with
+//     bf16 codes the zero point, are applied to its 16 x 16 sums. That zero point needs
+//     sum x over the group, one more instruction with a constant operand, shared by the R
+//     tiles; int8 rows do without (5120 -> 32003 at 64 rows, groups of 64: 44 -> 38 us);
 //   * x operands come straight from global memory (L2) in operand layout, 16 rows x 64
 //     (8-bit: 32) bytes a load, as many chunks ahead as the codes: the counter that
 //     loads retire by is in order, a shallower x ring would wait for the codes behind it.
@@ -60,11 +61,13 @@ struct Rows<kRowBf16> {
   typedef uint4 Wide;  // 8 elements as multiplied
   typedef f32x4_t Acc;
   static constexpr int kBytes = 2;
+  static constexpr bool kBiased = true;  // codes are multiplied as they are, 0 .. 15
   static __device__ __forceinline__ Op load(__amdgpu_buffer_rsrc_t rs, uint32_t at, uint32_t s) {
     return buf_load16(rs, at, s);
   }
   static __device__ __forceinline__ Wide widen(const Op& x) { return x; }
-  static __device__ __forceinline__ Wide codes(uint32_t w) {
+  template <bool ZERO>
+  static __device__ __forceinline__ Wide codes(uint32_t w, uint32_t) {
     const uint32_t lo = w & 0x0F0F0F0Fu, hi = (w >> 4) & 0x0F0F0F0Fu;
     return Wide{bf16_of_e4m3<false>(lo, 512.f), bf16_of_e4m3<true>(lo, 512.f), bf16_of_e4m3<false>(hi, 512.f),
                 bf16_of_e4m3<true>(hi, 512.f)};
@@ -97,10 +100,16 @@ struct Rows<kRowI8> {
     return buf_load8(rs, at, s);
   }
   static __device__ __forceinline__ Wide widen(const Op& x) { return x; }
-  static __device__ __forceinline__ Wide codes(uint32_t w) { return Wide{w & 0x0F0F0F0Fu, (w >> 4) & 0x0F0F0F0Fu}; }
-  static __device__ __forceinline__ Wide minus(bool eight) {
-    const uint32_t v = eight ? 0xF8F8F8F8u : 0xFFFFFFFFu;
-    return Wide{v, v};
+  // Codes less their zero point (z in every byte of zeros), as two's complement bytes: with
+  // bit 7 set first no byte borrows from the next. Without zero points 16 (c - 8), which is
+  // the nibble in the byte's upper half with the sign turned.
+  static constexpr bool kBiased = false;
+  template <bool ZERO>
+  static __device__ __forceinline__ Wide codes(uint32_t w, uint32_t zeros) {
+    constexpr uint32_t kSign = 0x80808080u;
+    if constexpr (!ZERO) return Wide{((w << 4) & 0xF0F0F0F0u) ^ kSign, (w & 0xF0F0F0F0u) ^ kSign};
+    const uint32_t lo = (w & 0x0F0F0F0Fu) | kSign, hi = ((w >> 4) & 0x0F0F0F0Fu) | kSign;
+    return Wide{(lo - zeros) ^ kSign, (hi - zeros) ^ kSign};
   }
   static __device__ __forceinline__ Acc mma(const Wide& x, const Wide& w, const Acc& c) {
     return __builtin_amdgcn_mfma_i32_16x16x32_i8(__builtin_bit_cast(long, x), __builtin_bit_cast(long, w), c, 0, 0, 0);
@@ -131,25 +140,30 @@ __device__ __forceinline__ void spread(uint32_t v, uint32_t (&o)[GP]) {
   }
 }
 
-// Scales and zero points of a chunk's groups as floats, from the lane's raw ones.
-template <int GP, bool ZERO>
-__device__ __forceinline__ void group_factors(uint32_t scale, uint32_t zero, float (&s)[GP], float (&z)[GP]) {
+// Scales and zero points of a chunk's groups from the lane's raw ones, the zero points
+// as floats or, where they are taken off the codes, in every byte of a word.
+template <class X, int GP, bool ZERO>
+__device__ __forceinline__ void group_factors(uint32_t scale, uint32_t zero, float (&s)[GP], uint32_t (&z)[GP]) {
   uint32_t v[GP];
   spread<GP>(scale | zero << 16, v);
 #pragma unroll
   for (int j = 0; j < GP; ++j) {
     s[j] = __uint_as_float(v[j] << 16);
-    z[j] = ZERO ? static_cast<float>(v[j] >> 16) : 0.f;
+    if (X::kBiased) z[j] = ZERO ? __float_as_uint(static_cast<float>(v[j] >> 16)) : 0u;
+    else if (ZERO) z[j] = (v[j] >> 16) * 0x01010101u;
+    else s[j] *= 0.0625f, z[j] = 0u;
   }
 }
 
 // tot += s (acc + z xs) of a 16 x 16 block, xs holding -sum x (without zero points
-// -8 sum x, and z is not used).
-template <bool ZERO, typename Acc>
-__device__ __forceinline__ void add_group(const Acc& acc, const Acc& xs, float s, float z, float (&tot)[4]) {
+// -8 sum x, and z is not used); tot += s acc where the codes have no bias.
+template <class X, bool ZERO>
+__device__ __forceinline__ void add_group(const typename X::Acc& acc, const typename X::Acc& xs, float s, uint32_t z,
+                                          float (&tot)[4]) {
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    const float u = ZERO ? static_cast<float>(acc[e]) + z * static_cast<float>(xs[e]) : static_cast<float>(acc[e] + xs[e]);
+    float u = static_cast<float>(acc[e]);
+    if constexpr (X::kBiased) u = ZERO ? u + __uint_as_float(z) * xs[e] : u + xs[e];
     tot[e] += s * u;
   }
 }
@@ -215,26 +229,28 @@ __global__ __launch_bounds__(W * 64) void w4_matvec_kernel(int T, int K, const u
   for (int r = 0; r < R; ++r)
 #pragma unroll
     for (int e = 0; e < 4; ++e) tot[r][e] = 0.f;
-  const typename X::Wide minus = X::minus(!ZERO);
+  typename X::Wide minus{};
+  if constexpr (X::kBiased) minus = X::minus(!ZERO);
   auto step = [&](int i, const Chunk& c) {
     const bool absent = GP > 1 && (wave + W * i) * 128 + 64 == K && g >= 2;  // the lane's group
-    float s[R][GP], z[R][GP];
+    float s[R][GP];
+    uint32_t z[R][GP];
 #pragma unroll
-    for (int r = 0; r < R; ++r) group_factors<GP, ZERO>(absent ? 0u : c.scale[r], ZERO ? c.zero[r] : 0u, s[r], z[r]);
+    for (int r = 0; r < R; ++r) group_factors<X, GP, ZERO>(absent ? 0u : c.scale[r], ZERO ? c.zero[r] : 0u, s[r], z[r]);
     Acc acc[R], xs;
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       const bool first = q * 32 % G == 0;
       const typename X::Wide xq = X::widen(c.x[q]);
-      xs = X::mma(xq, minus, first ? Acc{} : xs);
+      if constexpr (X::kBiased) xs = X::mma(xq, minus, first ? Acc{} : xs);
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         const uint32_t words[4] = {c.codes[r].x, c.codes[r].y, c.codes[r].z, c.codes[r].w};
-        acc[r] = X::mma(xq, X::codes(words[q]), first ? Acc{} : acc[r]);
+        acc[r] = X::mma(xq, X::template codes<ZERO>(words[q], z[r][q * 32 / G]), first ? Acc{} : acc[r]);
       }
       if ((q + 1) * 32 % G == 0) {
 #pragma unroll
-        for (int r = 0; r < R; ++r) add_group<ZERO>(acc[r], xs, s[r][q * 32 / G], z[r][q * 32 / G], tot[r]);
+        for (int r = 0; r < R; ++r) add_group<X, ZERO>(acc[r], xs, s[r][q * 32 / G], z[r][q * 32 / G], tot[r]);
       }
     }
   };
@@ -363,7 +379,8 @@ __global__ __launch_bounds__(RW * KW * 64) void w4_matvec_shared_kernel(int64_t 
     for (int b = 0; b < TB; ++b)
 #pragma unroll
       for (int j = 0; j < 4; ++j) tot[r][b][j] = 0.f;
-  const typename X::Wide minus = X::minus(!ZERO);
+  typename X::Wide minus{};
+  if constexpr (X::kBiased) minus = X::minus(!ZERO);
   // operand q of row block b: 8 elements at 32 q + 8 g of row 16 b + l16
   auto x_op = [&](const unsigned char* chunk, int b, int q) {
     const int row = 16 * b + l16, byte = (32 * q + 8 * g) * X::kBytes;
@@ -375,9 +392,10 @@ __global__ __launch_bounds__(RW * KW * 64) void w4_matvec_shared_kernel(int64_t 
     if (at >= kt) return;  // the last step may lack a chunk
     const bool absent = has_half && at == kt - 1 && g >= 2;  // the lane's group
     const unsigned char* const chunk = stage + kw * kChunk;
-    float s[R][GP], z[R][GP];
+    float s[R][GP];
+    uint32_t z[R][GP];
 #pragma unroll
-    for (int r = 0; r < R; ++r) group_factors<GP, ZERO>(absent ? 0u : c.scale[r], ZERO ? c.zero[r] : 0u, s[r], z[r]);
+    for (int r = 0; r < R; ++r) group_factors<X, GP, ZERO>(absent ? 0u : c.scale[r], ZERO ? c.zero[r] : 0u, s[r], z[r]);
     Acc acc[R][TB], xs[TB];
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
@@ -386,12 +404,12 @@ __global__ __launch_bounds__(RW * KW * 64) void w4_matvec_shared_kernel(int64_t 
 #pragma unroll
       for (int b = 0; b < TB; ++b) {
         xq[b] = X::widen(x_op(chunk, b, q));
-        xs[b] = X::mma(xq[b], minus, first ? Acc{} : xs[b]);
+        if constexpr (X::kBiased) xs[b] = X::mma(xq[b], minus, first ? Acc{} : xs[b]);
       }
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         const uint32_t words[4] = {c.codes[r].x, c.codes[r].y, c.codes[r].z, c.codes[r].w};
-        const typename X::Wide w = X::codes(words[q]);
+        const typename X::Wide w = X::template codes<ZERO>(words[q], z[r][q * 32 / G]);
 #pragma unroll
         for (int b = 0; b < TB; ++b) acc[r][b] = X::mma(xq[b], w, first ? Acc{} : acc[r][b]);
       }
@@ -400,7 +418,7 @@ __global__ __launch_bounds__(RW * KW * 64) void w4_matvec_shared_kernel(int64_t 
 #pragma unroll
         for (int r = 0; r < R; ++r)
 #pragma unroll
-          for (int b = 0; b < TB; ++b) add_group<ZERO>(acc[r][b], xs[b], s[r][j], z[r][j], tot[r][b]);
+          for (int b = 0; b < TB; ++b) add_group<X, ZERO>(acc[r][b], xs[b], s[r][j], z[r][j], tot[r][b]);
       }
     }
   };
