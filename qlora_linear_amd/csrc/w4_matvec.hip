@@ -309,9 +309,16 @@ __global__ __launch_bounds__(RW * KW * 64) void w4_matvec_shared_kernel(int64_t 
   __shared__ __align__(1024) unsigned char slot0[kStage];
   __shared__ __align__(1024) unsigned char slot1[kStage];
   __shared__ __align__(1024) unsigned char slot2[kStage];
-  __shared__ float sums[KW > 1 ? KW - 1 : 1][RW][R * TB * 4][64];
   const int lane = threadIdx.x & 63, l16 = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), rw = wave % RW, kw = wave / RW;
+  // When the last step is over the chunk waves' sums meet in the slots: value i of a wave
+  // (64 lanes) beside those of the other row waves.
+  constexpr int kSumsOf = kStage / 4 / (RW * 64);  // values a slot holds
+  static_assert((KW - 1) * R * TB * 4 <= NS * kSumsOf, "sums fit the slots");
+  auto sums = [&](int i) -> float& {
+    unsigned char* const slot = i / kSumsOf == 0 ? slot0 : i / kSumsOf == 1 ? slot1 : slot2;
+    return reinterpret_cast<float*>(slot)[(i % kSumsOf * RW + rw) * 64 + lane];
+  };
   const int sp = blockIdx.x % splits;
   const int64_t t0 = static_cast<int64_t>(blockIdx.x / splits % t_blocks) * (16 * TB);
   int group = blockIdx.x / splits / t_blocks, p = 0;
@@ -452,15 +459,18 @@ __global__ __launch_bounds__(RW * KW * 64) void w4_matvec_shared_kernel(int64_t 
     if (i + 1 < steps) turn(i + 1, ring[1], slot1, slot0);
     if (i + 2 < steps) turn(i + 2, ring[2], slot2, slot1);
   }
-  wait_vmem();  // run-ahead copies land before the workgroup gives its LDS back
+  wait_vmem();  // run-ahead copies land before their slots are used again or given back
   if constexpr (KW > 1) {
-    if (kw > 0) {
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < KW - 1; ++k) {
+      if (kw != k + 1) continue;
 #pragma unroll
       for (int r = 0; r < R; ++r)
 #pragma unroll
         for (int b = 0; b < TB; ++b)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) sums[kw - 1][rw][(r * TB + b) * 4 + e][lane] = tot[r][b][e];
+          for (int e = 0; e < 4; ++e) sums((k * R * TB + r * TB + b) * 4 + e) = tot[r][b][e];
     }
     __syncthreads();
     if (kw > 0) return;
@@ -485,7 +495,7 @@ __global__ __launch_bounds__(RW * KW * 64) void w4_matvec_shared_kernel(int64_t 
           float v = tot[r][b][e];
           if constexpr (KW > 1)
 #pragma unroll
-            for (int k = 0; k < KW - 1; ++k) v += sums[k][rw][(r * TB + b) * 4 + e][lane];
+            for (int k = 0; k < KW - 1; ++k) v += sums((k * R * TB + r * TB + b) * 4 + e);
           v *= factor[b][e];
           if (t < T && n < N) {
             if constexpr (sizeof(*y) == 2) y[t * stride + n] = to_bf16(v);
@@ -604,7 +614,7 @@ hipError_t run_shared(Call c) {
 // Which kernel, and over how many workgroups d_in is split (their float32 sums meet in
 // the workspace and a second launch joins them, about 2 us). Measured (us):
 //   * up to 16 rows. Over 768 tiles there are workgroups enough: four tiles each (8192 ->
-//     28672 at 1 row 27; two tiles and 16 waves 32). Fewer tiles at a usual depth: two tiles
+//     28672 at 1 row 26; two tiles and 16 waves 32). Fewer tiles at a usual depth: two tiles
 //     over 16 waves (4096 -> 6144 at 4 rows 5.9; one tile 6.9), one tile below 257 (4096 ->
 //     1024 at 1 row 4.2; two 4.9). From 96 chunks with few tiles, x in LDS and d_in split
 //     (28672 -> 8192 at 16 rows 33, 28672 -> 1024 at 16 rows 14; two tiles over 16 waves 40
@@ -653,7 +663,9 @@ hipError_t pick(Kind kind, const Call& c) {
     case kTwoTiles: return run<XT, 2, 16, 2>(c);
     case kFourTiles: return run<XT, 4, 8, 1>(c);
     case kDeep: return run_shared<XT, 1, 1, 4, 4>(c);
-    case kWide32: return run_shared<XT, 2, 2, 4, 2>(c);
+    // (16 waves where the ring is half as wide: 8192 -> 28672 at 32 int8 rows 39 us, with 8 44;
+    // bf16 rows 38 with 8, 36 to 47 with 16, where an instance spills)
+    case kWide32: return run_shared<XT, 2, 2, 4, XT == kRowBf16 ? 2 : 4>(c);
     case kWide64: return run_shared<XT, 4, 2, 4, 2>(c);
     case kNarrow: return run_shared<XT, 2, 1, 4, 2>(c);
   }
