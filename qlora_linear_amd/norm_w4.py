@@ -102,6 +102,12 @@ def _call(name, dev, *args):
         raise LoraNF4Error(name, st)
 
 
+def _workspace_on(dev, workspace):
+    if _dev(workspace, "workspace", torch.uint8).get_device() != dev:
+        raise ValueError(f"workspace must be a tensor on GPU {dev}")
+    return workspace
+
+
 def _call_matvec(name, dev, args, workspace, need, x):
     """A product on the caller's workspace, or on a new one of need() bytes where it turns out
     that one is needed (most shapes take none, and asking costs as much as trying)."""
@@ -111,7 +117,7 @@ def _call_matvec(name, dev, args, workspace, need, x):
             workspace = x.new_empty(need(), dtype=torch.uint8)
             st = _status(name, dev, (*args, workspace.data_ptr(), workspace.numel()))
     else:
-        _dev(workspace, "workspace", torch.uint8)
+        _workspace_on(dev, workspace)
         st = _status(name, dev, (*args, workspace.data_ptr(), workspace.numel()))
     if st != LN_OK:
         raise LoraNF4Error(name, st)
@@ -167,6 +173,8 @@ def rmsnorm_bwd(dy, h, weight, rstd, dh=None, need_dw: bool = True, workspace: t
     e = None if dh is None else _at(dh, "dh", dev, h.dtype, (T, d))
     dx = torch.empty_like(h)
     dw = torch.empty_like(weight) if need_dw else None
+    if workspace is not None:
+        _workspace_on(dev, workspace)
     ws = _workspace(rmsnorm_bwd_workspace_bytes(T, d), workspace, h.device) if need_dw else None
     _call("rmsnorm_bwd", dev, T, d, kind, g, e, h.data_ptr(), w, r, dx.data_ptr(),
           None if dw is None else dw.data_ptr(), None if ws is None else ws.data_ptr(),
