@@ -215,6 +215,20 @@ def test_w4_matvec_exact_on_integers(q, T, K, N, group, zero_points, kind):
     assert np.array_equal(host(y), x @ W.T)
 
 
+@pytest.mark.parametrize("kind", ["bf16", "e4m3", "i8"])
+@pytest.mark.parametrize("zero_points", [False, True])
+@pytest.mark.parametrize("T,K,N,group", [(17, 1856, 24580, 64), (32, 2176, 24580, 128), (50, 1088, 24580, 32)])
+def test_w4_matvec_wide_many_steps(q, T, K, N, group, zero_points, kind):
+    """Weights wide enough for one block of rows, d_in of several turns of the ring with a
+    last step that lacks chunks or half of one. Exact, as above."""
+    print("w4_matvec wide", T, K, N, group, zero_points, kind, flush=True)
+    codes, scales, zeros, W = packed(T + K, N, K, group, zero_points, pow2=True)
+    x = np.random.default_rng(K).integers(-3, 4, size=(T, K)).astype(np.float64)
+    assert (np.abs(x) @ (np.abs(W).T + 15 * 4)).max() < 2 ** 22
+    y = q.w4_matvec(torch.from_numpy(x).float().to(XT[kind]).cuda(), codes, scales, zeros, d_out=N, dtype=F)
+    assert np.array_equal(host(y), x @ W.T)
+
+
 @pytest.mark.parametrize("out", [BF, F], ids=["bf16", "f32"])
 @pytest.mark.parametrize("kind", ["bf16", "e4m3", "i8"])
 @pytest.mark.parametrize("T,K,N,group", [(1, 4096, 300, 128), (6, 1344, 77, 64), (16, 2048, 96, 32), (64, 4096, 64, 128)])
