@@ -97,10 +97,10 @@ size_t rmsnorm_bwd_workspace_bytes(int64_t T, int64_t d);
 
 /*
  * w4_quantize — packs w [d_out, d_in] (LN_F32 or LN_BF16), round to nearest-even:
- *   zeros NULL: s = bf16(f32(max|w| f32(1/7))),  c = clamp(rint(f32(w / s)), -8, 7) + 8
- *   zeros:      lo = min(w, 0), hi = max(w, 0) over the group, s = bf16(f32(f32(hi - lo) f32(1/15))),
+ *   zeros NULL: s = bf16(f32(max|w| / 7)),  c = clamp(rint(f32(w / s)), -8, 7) + 8
+ *   zeros:      lo = min(w, 0), hi = max(w, 0) over the group, s = bf16(f32(f32(hi - lo) / 15)),
  *               z = clamp(rint(f32(-lo / s)), 0, 15),  c = clamp(rint(f32(w / s)) + z, 0, 15)
- * A group with s = 0 has c = z (8, or 0 with zero points).
+ * A group with s = 0 has c = z (8, or 0 with zero points). hi - lo must be finite in float32.
  */
 int w4_quantize(const void* w, int w_dtype, int64_t d_out, int64_t d_in, int32_t group, uint8_t* codes,
                 uint16_t* scales, uint8_t* zeros, void* stream);

@@ -52,11 +52,11 @@ def w4_quantize(w, group, zero_points):
     g = w.reshape(N, K // group, group)
     if zero_points:
         lo, hi = np.minimum(g.min(2), 0), np.maximum(g.max(2), 0)
-        s = to_bf16((hi - lo) * np.float32(1 / 15))
+        s = to_bf16((hi - lo) / np.float32(15))
         z = np.divide(-lo, s, out=np.zeros_like(s), where=s > 0)
         z = np.clip(np.rint(z), 0, 15)
     else:
-        s = to_bf16(np.abs(g).max(2) * np.float32(1 / 7))
+        s = to_bf16(np.abs(g).max(2) / np.float32(7))
         z = np.full_like(s, 8)
     v = np.divide(g, s[..., None], out=np.zeros_like(g), where=s[..., None] > 0)
     c = np.clip(np.rint(v) + z[..., None], 0, 15)
