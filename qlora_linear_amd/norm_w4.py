@@ -6,7 +6,7 @@ a 4-bit group-scaled weight.
     dx, dw = rmsnorm_bwd(dy, h, w, rstd, dh=dh)                   # dx: of x and of res
     q, scale, h = rmsnorm_fwd_quant(x, w, residual=res)           # 8-bit rows, one scale each
     packed = w4_quantize(lora_nf4_merge(codes, absmax, A, B, lora_alpha), group=128)
-    y = w4_matvec(q, *packed, d_out=d_out, x_scale=scale)         # (codes, scales, zeros)
+    y = w4_matvec(q, *packed, d_out=d_out, x_scale=scale, group=128)   # (codes, scales, zeros)
 
 Like the rest of the binding these functions only check and marshal their arguments,
 allocate the outputs and call the C entry point of the same name on the current stream
@@ -200,14 +200,30 @@ def w4_quantize(w, group: int = 128, zero_points: bool = False):
     return codes, scales, zeros
 
 
-def _packed(codes, scales, zeros, d_in, d_out, dev, index=None):
+# A packed weight's tensors do not hold its width: 64 columns fill half a tile, and with groups
+# of 32 (64) they have the shapes of 128 columns with groups of 64 (128).
+
+def _columns(codes, scales, group):
+    """d_in of a packed weight from its shapes, and its group size if given."""
+    if not isinstance(scales, torch.Tensor) or scales.dim() != 3 or not scales.shape[1]:
+        raise ValueError("scales must be [ceil(d_out / 16), d_in / group, 16]")
+    full, kg = codes.shape[1] * 128, scales.shape[1]
+    fits = [k for k in (full, full - 64) if k % kg == 0 and k // kg in _GROUPS and group in (None, k // kg)]
+    if len(fits) != 1:
+        raise ValueError(f"{codes.shape[1]} tiles and {kg} groups of a row with group {group} " +
+                         ("are 64 or 128 columns: give d_in or group" if fits else "are no packed weight"))
+    return fits[0]
+
+
+def _packed(codes, scales, zeros, d_in, d_out, dev, index=None, want=None):
     """(d_out, group, addresses) of a packed weight whose rows are d_in wide; index: its
-    place in a list, for errors."""
+    place in a list, for errors; want: the group size that it must have."""
     try:
         nt, kg, rows = scales.shape
         group = d_in // kg
         n = 16 * nt if d_out is None else d_out
         if rows == 16 and group in _GROUPS and kg * group == d_in and 16 * (nt - 1) < n <= 16 * nt and \
+                want in (None, group) and \
                 scales.dtype is torch.bfloat16 and scales.get_device() == dev and scales.is_contiguous() and \
                 codes.dtype is torch.uint8 and codes.shape == (nt, (d_in + 127) // 128, 1024) and \
                 codes.get_device() == dev and codes.is_contiguous():
@@ -224,6 +240,8 @@ def _packed(codes, scales, zeros, d_in, d_out, dev, index=None):
     nt, kg, _ = scales.shape
     if kg * (d_in // kg) != d_in or d_in // kg not in _GROUPS:
         raise ValueError(f"scales{tag} hold {kg} groups of a row: d_in {d_in} makes no group of 32, 64 or 128")
+    if want is not None and want * kg != d_in:
+        raise ValueError(f"scales{tag} hold {kg} groups of a row: {want} columns each are not d_in {d_in}")
     if d_out is not None and not 16 * (nt - 1) < d_out <= 16 * nt:
         raise ValueError(f"d_out{tag} {d_out} does not fit scales{tag} of {nt} tiles of 16 rows")
     _at(scales, f"scales{tag}", dev, torch.bfloat16, (nt, kg, 16))
@@ -233,13 +251,14 @@ def _packed(codes, scales, zeros, d_in, d_out, dev, index=None):
 
 
 def w4_dequantize(codes, scales, zeros=None, *, d_out: int | None = None, d_in: int | None = None,
-                  dtype=torch.bfloat16):
-    """[d_out, d_in] float32 or bf16 values of a packed weight (defaults: every row and column
-    that the tiles hold)."""
+                  dtype=torch.bfloat16, group: int | None = None):
+    """[d_out, d_in] float32 or bf16 values of a packed weight. Defaults: every row that the
+    tiles hold, and the d_in that the shapes stand for; where they stand for 64 columns as
+    well as for 128 (one tile a row with one or two groups), d_in or group has to be given."""
     dev = _lead(codes, "codes", 3)
     kind = _code(_PLAIN, dtype, "dtype")
-    K = codes.shape[1] * 128 if d_in is None else d_in
-    N, group, c, s, z = _packed(codes, scales, zeros, K, d_out, dev)
+    K = _columns(codes, scales, group) if d_in is None else d_in
+    N, group, c, s, z = _packed(codes, scales, zeros, K, d_out, dev, None, group)
     out = codes.new_empty((N, K), dtype=dtype)
     _call("w4_dequantize", dev, c, s, z, N, K, group, kind, out.data_ptr())
     return out
@@ -261,13 +280,16 @@ def w4_matvec_multi_workspace_bytes(T: int, d_in: int, d_outs) -> int:
 
 
 def w4_matvec(x, codes, scales, zeros=None, *, d_out: int | None = None, x_scale=None, dtype=torch.bfloat16,
-              out=None, workspace: torch.Tensor | None = None):
+              out=None, workspace: torch.Tensor | None = None, group: int | None = None):
     """y = (x_scale x) W^T [T, d_out] in dtype (float32 or bf16) for x [T, d_in] bf16, float8_e4m3fn
     or int8 and a packed weight; x_scale: float32 [T] or None. Made for up to 64 rows. A workspace is
-    allocated where one is needed (w4_matvec_workspace_bytes) and none is given."""
+    allocated where one is needed (w4_matvec_workspace_bytes) and none is given.
+    x's width is the weight's d_in; the shapes alone cannot tell a weight of 64 columns from one
+    of 128 with groups twice as large, so where that may be mixed up give the group size too: a
+    weight of other groups is then refused."""
     dev, xt, xs, yt = _x_args(x, x_scale, dtype)
     T, K = x.shape
-    N, group, c, s, z = _packed(codes, scales, zeros, K, d_out, dev)
+    N, group, c, s, z = _packed(codes, scales, zeros, K, d_out, dev, None, group)
     if out is None:
         out = x.new_empty((T, N), dtype=dtype)
         y = out.data_ptr()
@@ -279,7 +301,7 @@ def w4_matvec(x, codes, scales, zeros=None, *, d_out: int | None = None, x_scale
 
 
 def w4_matvec_multi(x, codes, scales, zeros=None, *, d_out=None, x_scale=None, dtype=torch.bfloat16,
-                    workspace: torch.Tensor | None = None):
+                    workspace: torch.Tensor | None = None, group: int | None = None):
     """[y_g] of several packed weights (lists, one entry per weight) that read the same x, as one
     w4_matvec each but together in one launch. zeros: None, or one entry per weight."""
     dev, xt, xs, yt = _x_args(x, x_scale, dtype)
@@ -289,7 +311,7 @@ def w4_matvec_multi(x, codes, scales, zeros=None, *, d_out=None, x_scale=None, d
             (d_out is not None and len(d_out) != n):
         raise ValueError(f"codes, scales (zeros, d_out) must be lists of the same length, 1 to {LN_MAX_PROJ}")
     N, groups, c, s, z = zip(*(_packed(codes[g], scales[g], None if zeros is None else zeros[g], K,
-                                       None if d_out is None else d_out[g], dev, g) for g in range(n)))
+                                       None if d_out is None else d_out[g], dev, g, group) for g in range(n)))
     if len(set(groups)) > 1:
         raise ValueError("all weights must share the group size")
     if not all(z) and any(z):

@@ -1,5 +1,5 @@
 """RMS norm and packed 4-bit weights on the GPU where they are easily wrong: scales at a
-rounding's border, against the float64 oracle."""
+rounding's border, weights of one tile, against the float64 oracle."""
 import numpy as np
 import pytest
 import torch
@@ -35,3 +35,34 @@ def test_w4_quantize_scale_next_to_a_tie(q, zero_points):
     assert np.array_equal(scales.float().cpu().numpy(), ps)
     assert np.array_equal(codes.cpu().numpy(), pc)
     assert not zero_points or np.array_equal(zeros.cpu().numpy(), pz)
+
+
+@pytest.mark.parametrize("zero_points", [False, True])
+@pytest.mark.parametrize("K,group", [(64, 32), (64, 64), (128, 64), (128, 128), (128, 32), (192, 64), (320, 32), (960, 64)])
+def test_packed_width_by_default(q, K, group, zero_points):
+    """Read back without d_in: every column, or an error where 64 and 128 columns have the
+    same shapes; never the values of another width."""
+    w = torch.randn(20, K, generator=torch.Generator().manual_seed(K)).cuda()
+    packed = q.w4_quantize(w, group, zero_points)
+    want = q.w4_dequantize(*packed, d_out=20, d_in=K, dtype=F)
+    if K // group <= 2 and K <= 128:
+        with pytest.raises(ValueError, match="d_in or group"):
+            q.w4_dequantize(*packed, d_out=20)
+    else:
+        assert torch.equal(q.w4_dequantize(*packed, d_out=20, dtype=F), want)
+    assert torch.equal(q.w4_dequantize(*packed, d_out=20, dtype=F, group=group), want)
+    x = torch.randn(3, K, device="cuda").bfloat16()
+    y = q.w4_matvec(x, *packed, d_out=20, dtype=F)
+    assert torch.equal(q.w4_matvec(x, *packed, d_out=20, dtype=F, group=group), y)
+    lists = [[t] for t in packed[:2]] + ([[packed[2]]] if zero_points else [None])
+    assert torch.equal(q.w4_matvec_multi(x, *lists, d_out=[20], dtype=F, group=group)[0], y)
+    for wrong in (group * 2, group // 2):
+        with pytest.raises(ValueError):
+            q.w4_matvec(x, *packed, d_out=20, group=wrong)
+    # x of the width that has the same shapes
+    other = torch.randn(3, K * 2 if K == 64 else K // 2, device="cuda").bfloat16()
+    for call in (lambda: q.w4_matvec(other, *packed, d_out=20, group=group),
+                 lambda: q.w4_matvec_multi(other, *lists, d_out=[20], group=group),
+                 lambda: q.w4_dequantize(*packed, d_out=20, d_in=other.shape[1], group=group)):
+        with pytest.raises(ValueError):
+            call()
