@@ -177,7 +177,38 @@ dim3 row_grid(int64_t n) {
 }
 __device__ __forceinline__ int64_t row_block() { return static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x; }
 
-constexpr float kTiny = 0x1p-100f, kUp = 0x1p64f;
+// A row's 8-bit scale and what turns its values into levels, from top = max |y|. top is
+// m rstd with m = max |h w|, which the reduction of the sum of squares finds beside it. h w may
+// leave float32's normal range where y = h rstd w does not: near its ends (and in rows of zeros)
+// top is found again, from y.
+constexpr float kTiny = 0x1p-100f, kUp = 0x1p64f, kHuge = 0x1p127f;
+__device__ __forceinline__ bool far_row(float m, float top) {
+  return __builtin_expect(!(fminf(m, top) >= kTiny && top <= kHuge), 0);
+}
+struct Levels {
+  float scale, up, inv;  // level = y * up * inv
+};
+template <int OUT>
+constexpr float kTopLevel = OUT == kRowE4m3 ? 448.f : 127.f;
+template <int OUT>
+__device__ __forceinline__ Levels row_levels(float top) {
+  return Levels{top / kTopLevel<OUT>, 1.f, kTopLevel<OUT> / top};
+}
+// The same for any top: rows so small that the reciprocal would overflow are scaled up first
+// (exactly). A subnormal scale has few bits: it is rounded up, so that no level passes the top
+// one, and the levels are those of the scale as it is then.
+template <int OUT>
+__device__ __forceinline__ Levels far_levels(float top) {
+  constexpr float kTop = kTopLevel<OUT>;
+  Levels l{top / kTop, top < kTiny ? kUp : 1.f, 0.f};
+  float over = kTop, under = top * l.up;
+  if (l.scale < 0x1p-126f) {
+    if (l.scale * kTop < top) l.scale = __uint_as_float(__float_as_uint(l.scale) + 1u);
+    over = 1.f, under = l.scale * kUp;
+  }
+  if (l.scale > 0.f) l.inv = over / under;  // (not of zeros, not NaN)
+  return l;
+}
 
 // ---- forward ---------------------------------------------------------------------------
 // 8192 x 4096 bf16 with residual 44 us, 6.1 TB/s; 1 x 4096 to E4M3 3 us, a launch and two
@@ -248,15 +279,25 @@ __global__ __launch_bounds__((TPR < 256 ? 256 : TPR)) void rmsnorm_fwd_kernel(
   row_reduce<TPR>(s, m, red);
   const float rstd = 1.0f / __builtin_sqrtf(s / static_cast<float>(d) + eps);
   if (i0 == 0 && rstd_out != nullptr) rstd_out[t] = rstd;
-  float up = 1.f, inv = 0.f;
+  Levels to{};
   if constexpr (kQuant) {
-    constexpr float kTop = OUT == kRowE4m3 ? 448.f : 127.f;
-    const float top = m * rstd, scale = top / kTop;
-    // levels are y times one reciprocal a row; rows so small that it would overflow are
-    // scaled up first (exactly)
-    up = top < kTiny ? kUp : 1.f;
-    inv = scale > 0.f ? kTop / (top * up) : 0.f;
-    if (i0 == 0) q_scale[t] = scale;
+    const float top = m * rstd;
+    to = row_levels<OUT>(top);
+    if (far_row(m, top)) {  // (the same in all threads of a row, and so of a workgroup with barriers)
+      float unused = 0.f, far = 0.f;
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        Held<E> wt = weight(v);
+        repack(hv[v]);
+        repack(wt);
+#pragma unroll
+        for (int j = 0; j < kN; ++j) far = fmaxf(far, fabsf(elem(hv[v], j) * rstd * elem(wt, j)));
+      }
+      if constexpr (TPR > 64) __syncthreads();  // red has been read
+      row_reduce<TPR>(unused, far, red);
+      to = far_levels<OUT>(top == top ? far : top);
+    }
+    if (i0 == 0) q_scale[t] = to.scale;
   }
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
@@ -269,7 +310,7 @@ __global__ __launch_bounds__((TPR < 256 ? 256 : TPR)) void rmsnorm_fwd_kernel(
     for (int j = 0; j < kN; ++j) f[j] = elem(hv[v], j) * rstd * elem(wt, j);
     if constexpr (kQuant) {
 #pragma unroll
-      for (int j = 0; j < kN; ++j) f[j] = f[j] * up * inv;
+      for (int j = 0; j < kN; ++j) f[j] = f[j] * to.up * to.inv;
       store_levels<OUT>(static_cast<uint8_t*>(y) + row + at, left, f);
     } else if (left > 0) {
       store_vec(static_cast<E*>(y) + row + at, left, hold<E>(f));
@@ -292,6 +333,7 @@ __global__ __launch_bounds__(kLoop) void rmsnorm_fwd_loop_kernel(int64_t T, int 
   const int64_t t = row_block(), row = t * d;
   if (t >= T) return;
   constexpr int kN = Vec<E>::kN;
+  constexpr bool kQuant = OUT == kRowE4m3 || OUT == kRowI8;
   auto h_at = [&](int at) {
     Held<E> v = load_vec(x + row + at, d - at);
     if (res == nullptr) return v;
@@ -313,9 +355,22 @@ __global__ __launch_bounds__(kLoop) void rmsnorm_fwd_loop_kernel(int64_t T, int 
   }
   row_reduce<kLoop>(s, m, red);
   const float rstd = 1.0f / __builtin_sqrtf(s / static_cast<float>(d) + eps);
-  constexpr float kTop = OUT == kRowE4m3 ? 448.f : 127.f;
-  const float top = m * rstd, scale = top / kTop, up = top < kTiny ? kUp : 1.f;
-  const float inv = scale > 0.f ? kTop / (top * up) : 0.f;
+  Levels to{};
+  if constexpr (kQuant) {
+    const float top = m * rstd;
+    to = row_levels<OUT>(top);
+    if (far_row(m, top)) {
+      float unused = 0.f, far = 0.f;
+      for (int at = threadIdx.x * kN; at < d; at += kLoop * kN) {
+        const Held<E> v = h_at(at), wt = load_vec(w + at, d - at);
+#pragma unroll
+        for (int j = 0; j < kN; ++j) far = fmaxf(far, fabsf(elem(v, j) * rstd * elem(wt, j)));
+      }
+      __syncthreads();  // red has been read
+      row_reduce<kLoop>(unused, far, red);
+      to = far_levels<OUT>(top == top ? far : top);
+    }
+  }
   for (int at = threadIdx.x * kN; at < d; at += kLoop * kN) {
     const int left = d - at;
     const Held<E> v = h_at(at), wt = load_vec(w + at, left);
@@ -323,9 +378,9 @@ __global__ __launch_bounds__(kLoop) void rmsnorm_fwd_loop_kernel(int64_t T, int 
     float f[kN];
 #pragma unroll
     for (int j = 0; j < kN; ++j) f[j] = elem(v, j) * rstd * elem(wt, j);
-    if constexpr (OUT == kRowE4m3 || OUT == kRowI8) {
+    if constexpr (kQuant) {
 #pragma unroll
-      for (int j = 0; j < kN; ++j) f[j] = f[j] * up * inv;
+      for (int j = 0; j < kN; ++j) f[j] = f[j] * to.up * to.inv;
       store_levels<OUT>(static_cast<uint8_t*>(y) + row + at, left, f);
     } else {
       store_vec(static_cast<E*>(y) + row + at, left, hold<E>(f));
@@ -333,7 +388,7 @@ __global__ __launch_bounds__(kLoop) void rmsnorm_fwd_loop_kernel(int64_t T, int 
   }
   if (threadIdx.x == 0) {
     if (rstd_out != nullptr) rstd_out[t] = rstd;
-    if (OUT == kRowE4m3 || OUT == kRowI8) q_scale[t] = scale;
+    if constexpr (kQuant) q_scale[t] = to.scale;
   }
 }
 
