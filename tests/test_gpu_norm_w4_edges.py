@@ -1,5 +1,6 @@
-"""RMS norm and packed 4-bit weights on the GPU where they are easily wrong: scales at a
-rounding's border, weights of one tile, rows far from 1, against the float64 oracle."""
+"""RMS norm and packed 4-bit weights on the GPU where they are easily wrong: many turns of
+the backward's row loop, offsets past 32 bits, scales at a rounding's border, weights of one
+tile, rows far from 1, stores between guard bands. Against the float64 oracle."""
 import numpy as np
 import pytest
 import torch
@@ -114,3 +115,156 @@ def test_rmsnorm_fwd_quant_far_values(q, T, d, far, dtype, fmt):
     v, s = y[~zero] / s[~zero, None], s[~zero, None]
     step = 0.5 if fmt == "i8" else np.maximum(2.0 ** -4 * np.abs(v), 2.0 ** -10)
     assert np.all(np.abs(got[~zero] - v) <= step + 1.1 * (4 * F32(d) * np.abs(v) + 2.0 ** -150 / s))
+
+
+HALF = {BF: 2.0 ** -8, F: 2.0 ** -24}
+
+
+def make(seed, *shape, dtype=BF):
+    return torch.randn(*shape, generator=torch.Generator().manual_seed(seed)).to(dtype)
+
+
+# More rows than one turn of the backward's workgroups takes, the last turn short: 512
+# workgroups of one row at 1024 threads a row, of two at 256, of eight at 64; rows read twice,
+# whose dw is summed by 64 workgroups along the rows.
+@pytest.mark.parametrize("dtype", [BF, F], ids=["bf16", "f32"])
+@pytest.mark.parametrize("T,d", [(5000, 200), (4200, 700), (1100, 2048), (1537, 4096), (600, 5003), (1100, 11008),
+                                 (130, 20000), (3, 1 << 20)])
+def test_rmsnorm_bwd_many_rows(q, T, d, dtype):
+    """Against the oracle, with dh and without, the weight learnt and frozen. A column of dw has
+    at most 80 additions one after another here: 10 turns of a thread, 8 rows of a workgroup, 16
+    of 512 workgroups and 32 sums of those."""
+    print("rmsnorm_bwd", T, d, dtype, flush=True)
+    h, w, dy, dh = make(7, T, d, dtype=dtype), make(8, d, dtype=dtype), make(9, T, d, dtype=dtype), make(10, T, d, dtype=dtype)
+    rstd = torch.from_numpy(o.rmsnorm(host(h), host(w), 1e-5)[1].astype(np.float32))
+    r = host(rstd)[:, None]
+    H, W, DY = host(h), host(w), host(dy)
+    g, n = DY * W, H * r
+    rx, rw = o.rmsnorm_grad(DY, H, W, r[:, 0])
+    mag = r * (np.abs(g) + np.abs(n) * np.abs(g * n).mean(1, keepdims=True))
+    wide = np.abs(DY * n).sum(0)
+    for e in (None, dh):
+        dev = [None if t is None else t.cuda() for t in (dy, h, w, rstd, e)]
+        dx, dw = q.rmsnorm_bwd(*dev[:4], dh=dev[4])
+        E = 0 if e is None else host(e)
+        assert np.all(np.abs(host(dx) - rx - E) <= HALF[dtype] * np.abs(rx + E) + F32(d) * (mag + np.abs(E)))
+        assert np.all(np.abs(host(dw) - rw) <= HALF[dtype] * np.abs(rw) + 80 * 2.0 ** -24 * wide)
+        frozen, none = q.rmsnorm_bwd(*dev[:4], dh=dev[4], need_dw=False)
+        assert none is None and torch.equal(frozen, dx)
+        again = q.rmsnorm_bwd(*dev[:4], dh=dev[4])
+        assert torch.equal(again[0], dx) and torch.equal(again[1], dw)
+
+
+def stream():
+    return torch.cuda.current_stream().cuda_stream
+
+
+@pytest.mark.parametrize("dtype", [BF, F], ids=["bf16", "f32"])
+@pytest.mark.parametrize("T,d", [(1, 1), (3, 7), (5, 1001), (600, 333), (1030, 2047), (2, 5003), (515, 8191), (70, 33333)])
+def test_norm_stores_stay_inside(q, T, d, dtype):
+    """Every output and the workspace, of exactly their size, between guard bands."""
+    from tests.gpu_util import Guarded
+    print("norm guards", T, d, dtype, flush=True)
+    lib, kind, e = q.library(), 1 if dtype == BF else 0, 2 if dtype == BF else 4
+    x, res, w, dh = (make(i, *s, dtype=dtype).cuda() for i, s in enumerate([(T, d), (T, d), (d,), (T, d)]))
+    h, y, rstd, lv, sc, dx, dw = (Guarded(n) for n in (T * d * e, T * d * e, T * 4, T * d, T * 4, T * d * e, d * e))
+    ws = Guarded(q.rmsnorm_bwd_workspace_bytes(T, d))
+    bufs = [h, y, rstd, lv, sc, dx, dw, ws]
+    assert lib.rmsnorm_fwd(T, d, kind, 1e-5, x.data_ptr(), res.data_ptr(), w.data_ptr(), h.ptr, y.ptr, rstd.ptr, stream()) == 0
+    want = q.rmsnorm_fwd(x, w, 1e-5, residual=res)
+    for got, t in zip((y, h, rstd), want):
+        assert torch.equal(got.view(t.dtype, t.shape), t)
+    for qt, qdtype in ((q.LN_E4M3, torch.float8_e4m3fn), (q.LN_I8, torch.int8)):
+        assert lib.rmsnorm_fwd_quant(T, d, kind, 1e-5, x.data_ptr(), res.data_ptr(), w.data_ptr(), h.ptr, qt, lv.ptr,
+                                     sc.ptr, stream()) == 0
+        a, b, c = q.rmsnorm_fwd_quant(x, w, 1e-5, residual=res, qdtype=qdtype)
+        assert torch.equal(lv.view(torch.uint8, (T, d)), a.view(torch.uint8)) and torch.equal(sc.view(F, (T,)), b)
+        assert torch.equal(h.view(dtype, (T, d)), c)
+    for learnt in (True, False):
+        assert lib.rmsnorm_bwd(T, d, kind, x.data_ptr(), dh.data_ptr(), want[1].data_ptr(), w.data_ptr(), want[2].data_ptr(),
+                               dx.ptr, dw.ptr if learnt else None, ws.ptr, ws.nbytes, stream()) == 0
+        rx, rw = q.rmsnorm_bwd(x, want[1], w, want[2], dh=dh)
+        assert torch.equal(dx.view(dtype, (T, d)), rx) and torch.equal(dw.view(dtype, (d,)), rw)
+    torch.cuda.synchronize()
+    assert all(b.canaries_intact() for b in bufs)
+
+
+@pytest.mark.parametrize("zero_points", [False, True])
+@pytest.mark.parametrize("N,K,group", [(1, 64, 32), (17, 192, 64), (40, 320, 32), (33, 384, 128)])
+def test_pack_stores_stay_inside(q, N, K, group, zero_points):
+    from tests.gpu_util import Guarded
+    print("pack guards", N, K, group, flush=True)
+    lib = q.library()
+    w = make(N, N, K).cuda()
+    want = q.w4_quantize(w, group, zero_points)
+    codes, scales, zeros, out = (Guarded(n) for n in (want[0].numel(), want[1].numel() * 2, want[1].numel(), N * K * 4))
+    z = zeros.ptr if zero_points else None
+    assert lib.w4_quantize(w.data_ptr(), 1, N, K, group, codes.ptr, scales.ptr, z, stream()) == 0
+    assert lib.w4_dequantize(codes.ptr, scales.ptr, z, N, K, group, 0, out.ptr, stream()) == 0
+    torch.cuda.synchronize()
+    assert all(b.canaries_intact() for b in (codes, scales, zeros, out))
+    for b, t in zip((codes, scales, zeros), want):
+        assert t is None or torch.equal(b.view(t.dtype, t.shape), t)
+    assert torch.equal(out.view(F, (N, K)), q.w4_dequantize(*want, d_out=N, d_in=K, dtype=F))
+
+
+# ---- offsets past 32 bits -----------------------------------------------------------
+def test_norm_past_32_bits(q):
+    """2.15e9 elements, 1025 rows again and again: every block of rows has the first one's bits."""
+    n, d, reps = 1025, 4096, 512
+    x, w, dy = make(1, n, d).cuda(), make(2, d).cuda(), make(3, n, d).cuda()
+    rows = lambda t: t.expand(reps, *t.shape).reshape(-1, *t.shape[1:])  # noqa: E731
+    X, DY = rows(x), rows(dy)
+    want = q.rmsnorm_fwd(x, w, residual=dy)
+    got = q.rmsnorm_fwd(X, w, residual=DY)
+    for a, b in zip(got, want):
+        assert torch.equal(a, rows(b))
+    lv, sc, _ = q.rmsnorm_fwd_quant(X, w)
+    a, b, _ = q.rmsnorm_fwd_quant(x, w)
+    assert torch.equal(lv.view(torch.uint8), rows(a.view(torch.uint8))) and torch.equal(sc, rows(b))
+    dx, dw = q.rmsnorm_bwd(DY, got[1], w, got[2])
+    assert torch.equal(dx, rows(q.rmsnorm_bwd(dy, want[1], w, want[2])[0]))
+    r = host(want[2])
+    terms = host(dy) * host(want[1]) * r[:, None]
+    # 513 turns of a thread, two rows of a workgroup, 16 of 512 workgroups and 32 sums of those
+    assert np.all(np.abs(host(dw) - reps * terms.sum(0)) <= HALF[BF] * np.abs(reps * terms.sum(0)) +
+                  570 * 2.0 ** -24 * reps * np.abs(terms).sum(0))
+
+
+def test_packing_past_32_bits(q):
+    """2.4e9 elements packed and read back: 1024 rows again and again."""
+    n, K, reps = 1024, 4096, 576
+    w = make(4, n, K).cuda()
+    W = w.expand(reps, n, K).reshape(-1, K)
+    want = q.w4_quantize(w, 64, True)
+    got = q.w4_quantize(W, 64, True)
+    for a, b in zip(got, want):
+        assert torch.equal(a, b.expand(reps, *b.shape).reshape(a.shape))
+    assert torch.equal(q.w4_dequantize(*got, d_in=K), q.w4_dequantize(*want, d_in=K).expand(reps, n, K).reshape(-1, K))
+
+
+@pytest.mark.parametrize("kind", [BF, torch.int8], ids=["bf16", "i8"])
+@pytest.mark.parametrize("T", [3, 20, 64])
+def test_w4_matvec_past_32_bits(q, T, kind):
+    """4.6e9 bytes of codes: 1024 rows of weight again and again. x small integers, scales
+    powers of two: exact in float32 in any order."""
+    n, K, group, reps = 1024, 8192, 64, 1100
+    g = torch.Generator().manual_seed(T)
+    codes = torch.randint(0, 256, (n // 16, K // 128, 1024), generator=g, dtype=torch.uint8).cuda()
+    scales = (2.0 ** torch.randint(-2, 3, (n // 16, K // group, 16), generator=g)).to(BF).cuda()
+    zeros = torch.randint(0, 16, scales.shape, generator=g, dtype=torch.uint8).cuda()
+    x = torch.randint(-1, 2, (T, K), generator=g).to(kind).cuda()
+    W = q.w4_dequantize(codes, scales, zeros, d_in=K, dtype=F)
+    want = host(x) @ host(W).T
+    assert (np.abs(host(x)) @ (np.abs(host(W)).T + 60)).max() < 2 ** 22
+    y = q.w4_matvec(x, *(t.expand(reps, *t.shape).reshape(-1, *t.shape[1:]) for t in (codes, scales, zeros)), dtype=F)
+    assert np.array_equal(host(y[:, :n]), want)
+    assert torch.equal(y, y[:, :n].repeat(1, reps))
+
+
+def test_w4_matvec_empty_batch(q):
+    packed = q.w4_quantize(make(5, 40, 256).cuda(), 64, True)
+    x = torch.empty(0, 256, dtype=BF, device="cuda")
+    assert q.w4_matvec(x, *packed, d_out=40).shape == (0, 40)
+    ys = q.w4_matvec_multi(x, [packed[0]] * 2, [packed[1]] * 2, [packed[2]] * 2, d_out=(40, 33))
+    assert [y.shape for y in ys] == [(0, 40), (0, 33)]
