@@ -11,7 +11,9 @@ a 4-bit group-scaled weight.
 Like the rest of the binding these functions only check and marshal their arguments,
 allocate the outputs and call the C entry point of the same name on the current stream
 of the tensors' device. They make one launch or two each and may be captured into a
-graph. Gradients are functions of their own, not autograd nodes.
+graph. Gradients are functions of their own, not autograd nodes. Matrices start on 16-byte
+boundaries, as PyTorch allocates them (a part of the rows of one does if a row is a multiple of
+16 bytes; otherwise it is refused).
 """
 from __future__ import annotations
 
@@ -84,6 +86,17 @@ def _at(t, name, dev, dtype, shape):
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     raise ValueError(f"{name} must be contiguous")
+
+
+def _row_factors(t, name, dev, T):
+    """The address of one float32 a row, and the tensor that holds it: part of a batch's
+    (scale[3:5]) may start anywhere, the C entry points take 16-byte boundaries, so such a
+    part is copied."""
+    at = _at(t, name, dev, torch.float32, (T,))
+    if at & 15:
+        t = t.clone()
+        at = t.data_ptr()
+    return at, t
 
 
 def _status(name, dev, args):
@@ -169,7 +182,7 @@ def rmsnorm_bwd(dy, h, weight, rstd, dh=None, need_dw: bool = True, workspace: t
     T, d = h.shape
     w = _at(weight, "weight", dev, h.dtype, (d,))
     g = _at(dy, "dy", dev, h.dtype, (T, d))
-    r = _at(rstd, "rstd", dev, torch.float32, (T,))
+    r, rstd = _row_factors(rstd, "rstd", dev, T)
     e = None if dh is None else _at(dh, "dh", dev, h.dtype, (T, d))
     dx = torch.empty_like(h)
     dw = torch.empty_like(weight) if need_dw else None
@@ -266,8 +279,8 @@ def w4_dequantize(codes, scales, zeros=None, *, d_out: int | None = None, d_in: 
 
 def _x_args(x, x_scale, dtype):
     dev = _lead(x, "x", 2)
-    return dev, _code(_X, x.dtype, "x"), None if x_scale is None else \
-        _at(x_scale, "x_scale", dev, torch.float32, (x.shape[0],)), _code(_PLAIN, dtype, "dtype")
+    xs, held = (None, None) if x_scale is None else _row_factors(x_scale, "x_scale", dev, x.shape[0])
+    return dev, _code(_X, x.dtype, "x"), xs, held, _code(_PLAIN, dtype, "dtype")
 
 
 def w4_matvec_workspace_bytes(T: int, d_in: int, d_out: int) -> int:
@@ -287,7 +300,7 @@ def w4_matvec(x, codes, scales, zeros=None, *, d_out: int | None = None, x_scale
     x's width is the weight's d_in; the shapes alone cannot tell a weight of 64 columns from one
     of 128 with groups twice as large, so where that may be mixed up give the group size too: a
     weight of other groups is then refused."""
-    dev, xt, xs, yt = _x_args(x, x_scale, dtype)
+    dev, xt, xs, x_scale, yt = _x_args(x, x_scale, dtype)
     T, K = x.shape
     N, group, c, s, z = _packed(codes, scales, zeros, K, d_out, dev, None, group)
     if out is None:
@@ -304,7 +317,7 @@ def w4_matvec_multi(x, codes, scales, zeros=None, *, d_out=None, x_scale=None, d
                     workspace: torch.Tensor | None = None, group: int | None = None):
     """[y_g] of several packed weights (lists, one entry per weight) that read the same x, as one
     w4_matvec each but together in one launch. zeros: None, or one entry per weight."""
-    dev, xt, xs, yt = _x_args(x, x_scale, dtype)
+    dev, xt, xs, x_scale, yt = _x_args(x, x_scale, dtype)
     T, K = x.shape
     n = len(codes)
     if not 1 <= n <= LN_MAX_PROJ or len(scales) != n or (zeros is not None and len(zeros) != n) or \

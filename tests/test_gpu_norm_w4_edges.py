@@ -268,3 +268,31 @@ def test_w4_matvec_empty_batch(q):
     assert q.w4_matvec(x, *packed, d_out=40).shape == (0, 40)
     ys = q.w4_matvec_multi(x, [packed[0]] * 2, [packed[1]] * 2, [packed[2]] * 2, d_out=(40, 33))
     assert [y.shape for y in ys] == [(0, 40), (0, 33)]
+
+
+# ---- parts of a batch ---------------------------------------------------------------
+@pytest.mark.parametrize("rows", [slice(3, 5), slice(1, 7), slice(4, 8), slice(7, 8)])
+def test_part_of_a_batch(q, rows):
+    """Some rows of a batch with their scales, which need not start on a 16-byte boundary."""
+    packed = [q.w4_quantize(make(i, n, 256).cuda(), 64, True) for i, n in enumerate((40, 64))]
+    x, w = make(20, 8, 256).cuda(), make(21, 256).cuda()
+    lv, scale, _ = q.rmsnorm_fwd_quant(x, w)
+    want = q.w4_matvec(lv, *packed[0], d_out=40, x_scale=scale)
+    assert torch.equal(q.w4_matvec(lv[rows], *packed[0], d_out=40, x_scale=scale[rows]), want[rows])
+    lists = [[p[i] for p in packed] for i in range(3)]
+    both = q.w4_matvec_multi(lv, *lists, d_out=(40, 64), x_scale=scale)
+    part = q.w4_matvec_multi(lv[rows], *lists, d_out=(40, 64), x_scale=scale[rows])
+    assert all(torch.equal(a, b[rows]) for a, b in zip(part, both))
+    y, h, rstd = q.rmsnorm_fwd(x, w)
+    dx, _ = q.rmsnorm_bwd(y, h, w, rstd)
+    assert torch.equal(q.rmsnorm_bwd(y[rows], h[rows], w, rstd[rows])[0], dx[rows])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = q.w4_matvec(lv[rows], *packed[0], d_out=40, x_scale=scale[rows])
+    for i in range(4):
+        scale.copy_(torch.full_like(scale, 2.0 ** i))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, q.w4_matvec(lv, *packed[0], d_out=40, x_scale=scale)[rows])
+    with pytest.raises(ValueError, match="contiguous"):
+        q.w4_matvec(lv[:2], *packed[0], d_out=40, x_scale=scale[3:6:2])
