@@ -296,3 +296,73 @@ def test_part_of_a_batch(q, rows):
         assert torch.equal(out, q.w4_matvec(lv, *packed[0], d_out=40, x_scale=scale)[rows])
     with pytest.raises(ValueError, match="contiguous"):
         q.w4_matvec(lv[:2], *packed[0], d_out=40, x_scale=scale[3:6:2])
+
+
+# ---- product: several weights in every kernel, the narrowest d_in, many rows ---------
+def exact_case(q, seed, T, K, widths, group, zero_points, kind):
+    """Packed weights with scales that are powers of two, x of small integers: exact in float32
+    in any order of additions. (x, packed weights, float64 products)"""
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randint(-2, 3, (T, K), generator=g)
+    packs, want = [], []
+    for n in widths:
+        nt = (n + 15) // 16
+        codes = torch.randint(0, 256, (nt, (K + 127) // 128, 1024), generator=g, dtype=torch.uint8).cuda()
+        scales = (2.0 ** torch.randint(-2, 2, (nt, K // group, 16), generator=g)).to(BF).cuda()
+        zeros = torch.randint(0, 16, scales.shape, generator=g, dtype=torch.uint8).cuda() if zero_points else None
+        W = host(q.w4_dequantize(codes, scales, zeros, d_out=n, d_in=K, dtype=F))
+        X = x.numpy().astype(np.float64)
+        assert (np.abs(X) @ (np.abs(W).T + 30)).max() < 2 ** 22
+        packs.append((codes, scales, zeros))
+        want.append(X @ W.T)
+    return x.float().to(kind).cuda(), packs, want
+
+
+@pytest.mark.parametrize("kind", [BF, torch.float8_e4m3fn, torch.int8], ids=["bf16", "e4m3", "i8"])
+@pytest.mark.parametrize("zero_points", [False, True])
+@pytest.mark.parametrize("T,K,widths,group", [
+    (5, 16384, (200, 40, 1), 64), (1, 28672, (16, 300), 128),  # d_in split, up to 16 rows
+    (20, 4288, (40, 130, 7), 32), (70, 2176, (130, 33), 64),   # d_in split, more rows
+    (3, 192, (12300, 50, 17), 32), (16, 256, (3000, 2000), 128),
+    (33, 1088, (12000, 5000, 33), 64), (64, 1088, (20000, 4700), 32), (130, 64, (12000, 40), 64)])
+def test_w4_matvec_multi_exact(q, T, K, widths, group, zero_points, kind):
+    print("w4_matvec_multi exact", T, K, widths, group, zero_points, kind, flush=True)
+    x, packs, want = exact_case(q, T + K, T, K, widths, group, zero_points, kind)
+    lists = [[p[i] for p in packs] for i in range(3)]
+    factor = 2.0 ** torch.randint(-3, 4, (T,), generator=torch.Generator().manual_seed(T)).float()
+    for out in (F, BF):
+        ys = q.w4_matvec_multi(x, lists[0], lists[1], lists[2] if zero_points else None, d_out=widths,
+                               x_scale=factor.cuda(), dtype=out, group=group)
+        for y, w in zip(ys, want):
+            w = w * host(factor)[:, None]
+            assert np.array_equal(host(y), w if out == F else o.to_bf16(w).astype(np.float64))
+
+
+@pytest.mark.parametrize("kind", [BF, torch.float8_e4m3fn, torch.int8], ids=["bf16", "e4m3", "i8"])
+@pytest.mark.parametrize("T,K,N,group", [(1, 64, 40, 64), (20, 64, 40, 32), (64, 64, 24700, 64), (17, 128, 40, 128),
+                                         (33, 128, 3100, 32), (1000, 320, 100, 64), (4100, 128, 17, 128)])
+def test_w4_matvec_narrow_and_long(q, T, K, N, group, kind):
+    print("w4_matvec", T, K, N, group, kind, flush=True)
+    x, packs, want = exact_case(q, T + N, T, K, (N,), group, True, kind)
+    assert np.array_equal(host(q.w4_matvec(x, *packs[0], d_out=N, dtype=F)), want[0])
+
+
+@pytest.mark.parametrize("dtype", [BF, F], ids=["bf16", "f32"])
+def test_norm_of_millions_of_rows(q, dtype):
+    """More workgroups than lie along one side of a launch."""
+    T, d = 4300000, 5
+    x, res, w = make(1, T, d, dtype=dtype), make(2, T, d, dtype=dtype), make(3, d, dtype=dtype)
+    y, h, rstd = q.rmsnorm_fwd(x.cuda(), w.cuda(), residual=res.cuda())
+    assert torch.equal(h.cpu(), (x.float() + res.float()).to(dtype))
+    Y, r = o.rmsnorm(host(h), host(w), float(np.float32(1e-5)))
+    assert np.all(np.abs(host(rstd) - r) <= F32(d) * r)
+    assert np.all(np.abs(host(y) - Y) <= (HALF[dtype] + F32(d)) * np.abs(Y) + 1e-38)
+    lv, sc, _ = q.rmsnorm_fwd_quant(x.cuda(), w.cuda(), residual=res.cuda(), qdtype=torch.int8)
+    want = np.abs(Y).max(1) / 127
+    assert np.all(np.abs(host(sc) - want) <= F32(d) * want)
+    assert np.all(np.abs(host(lv) * want[:, None] - Y) <= 0.5 * want[:, None] + 4 * F32(d) * np.abs(Y))
+    dx, _ = q.rmsnorm_bwd(x.cuda(), h, w.cuda(), rstd, need_dw=False)
+    rx, _ = o.rmsnorm_grad(host(x), host(h), host(w), host(rstd))
+    g, n, r = host(x) * host(w), host(h) * host(rstd)[:, None], host(rstd)[:, None]
+    mag = r * (np.abs(g) + np.abs(n) * np.abs(g * n).mean(1, keepdims=True))
+    assert np.all(np.abs(host(dx) - rx) <= HALF[dtype] * np.abs(rx) + F32(d) * mag)
