@@ -218,6 +218,7 @@ __global__ __launch_bounds__((TPR < 256 ? 256 : TPR)) void rmsnorm_fwd_kernel(
     int64_t T, int d, float eps, const E* __restrict__ x, const E* __restrict__ res, const E* __restrict__ w,
     E* __restrict__ h, void* __restrict__ y, float* __restrict__ q_scale, float* __restrict__ rstd_out) {
   constexpr int kN = Vec<E>::kN, kBlock = TPR < 256 ? 256 : TPR;
+  static_assert(TPR == 64 || TPR == kBlock, "a barrier runs in workgroups of one row only");
   constexpr bool kQuant = OUT == kRowE4m3 || OUT == kRowI8;
   __shared__ float2 red[kBlock / 64];
   const int64_t t = row_block() * (kBlock / TPR) + threadIdx.x / TPR;
@@ -404,6 +405,7 @@ __global__ __launch_bounds__(BLOCK) void rmsnorm_bwd_kernel(int64_t T, int d, co
                                                             const float* __restrict__ rstd_in,
                                                             E* __restrict__ dx, float* __restrict__ part) {
   constexpr int kN = Vec<E>::kN, kSlots = BLOCK / TPR;
+  static_assert(TPR % 64 == 0 && BLOCK % TPR == 0, "whole waves a row, whole rows a workgroup");
   __shared__ float2 red[BLOCK / 64];
   const int i0 = threadIdx.x % TPR, slot = threadIdx.x / TPR;
   Held<E> wv[NV];
