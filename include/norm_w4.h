@@ -52,10 +52,12 @@ int rmsnorm_fwd(int64_t T, int64_t d, int dtype, float eps, const void* x, const
  * rmsnorm_fwd_quant — the same norm with its output in 8 bits and one scale a row, as
  * w4_matvec reads it:
  *     scale = max_j |y_j| / top,   q_j = y_j / scale in q_type    (top 448 or 127)
- * from the float32 y, rounded to nearest-even; a row of zeros has scale 0 and q 0. (The quotient
- * is formed as the product with one float32 reciprocal a row, a few 2^-24 of it off before
- * it is rounded to the level. A scale in float32's subnormal range is rounded up, so that no
- * level passes top; the levels are those of the scale as it is stored.)
+ * to the nearest level, halves to the even one; a row of zeros has scale 0 and q 0. The quotient
+ * y_j / scale is formed as (h w)_j (top / max |h w|), for bf16 rows exactly (h w is exact, and
+ * a quotient next to the middle of two levels is on its side of it), for float32 rows from
+ * the rounded h w and off by at most 3 2^-24 of it before it goes to its level. A scale in float32's
+ * subnormal range is rounded up, so that no level passes top; the levels are those of the
+ * scale as it is stored.
  *   q         [T, d] of q_type (LN_E4M3 or LN_I8), q_scale float32 [T] (outputs)
  *   the other arguments as for rmsnorm_fwd.
  */

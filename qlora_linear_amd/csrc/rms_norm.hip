@@ -177,31 +177,43 @@ dim3 row_grid(int64_t n) {
 }
 __device__ __forceinline__ int64_t row_block() { return static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x; }
 
-// A row's 8-bit scale and what turns its values into levels, from top = max |y|. top is
-// m rstd with m = max |h w|, which the reduction of the sum of squares finds beside it. h w may
-// leave float32's normal range where y = h rstd w does not: near its ends (and in rows of zeros)
-// top is found again, from y.
+// A row's 8-bit scale and what turns its values into levels. With m = max |h w|, which the
+// reduction of the sum of squares finds beside it, the scale is m rstd / top level and the level
+// of y is the nearest to h w (top level / m): rstd cancels. The factor is held in two parts, so
+// that the quotient is off by its last rounding only; with bf16 rows, whose h w is exact, a
+// quotient in the middle of two levels (1 in 10^4, as bf16 quotients have few bits) comes out
+// as that and goes to the even one.
+// h w may leave float32's normal range where y does not: near its ends (and in rows of zeros)
+// the largest y is found again, from y, and levels are y times a reciprocal of it.
 constexpr float kTiny = 0x1p-100f, kUp = 0x1p64f, kHuge = 0x1p127f;
 __device__ __forceinline__ bool far_row(float m, float top) {
   return __builtin_expect(!(fminf(m, top) >= kTiny && top <= kHuge), 0);
 }
 struct Levels {
-  float scale, up, inv;  // level = y * up * inv
+  float scale, first, inv, low;  // level = f inv + f low of f = h first w
+  template <int N>
+  __device__ __forceinline__ void apply(float (&f)[N]) const {
+#pragma unroll
+    for (int j = 0; j < N; ++j) f[j] = __builtin_fmaf(f[j], inv, f[j] * low);
+  }
 };
 template <int OUT>
 constexpr float kTopLevel = OUT == kRowE4m3 ? 448.f : 127.f;
 template <int OUT>
-__device__ __forceinline__ Levels row_levels(float top) {
-  return Levels{top / kTopLevel<OUT>, 1.f, kTopLevel<OUT> / top};
-}
-// The same for any top: rows so small that the reciprocal would overflow are scaled up first
-// (exactly). A subnormal scale has few bits: it is rounded up, so that no level passes the top
-// one, and the levels are those of the scale as it is then.
-template <int OUT>
-__device__ __forceinline__ Levels far_levels(float top) {
+__device__ __forceinline__ Levels row_levels(float m, float top) {
   constexpr float kTop = kTopLevel<OUT>;
-  Levels l{top / kTop, top < kTiny ? kUp : 1.f, 0.f};
-  float over = kTop, under = top * l.up;
+  const float inv = kTop / m;
+  return Levels{top / kTop, 1.f, inv, __builtin_fmaf(-inv, m, kTop) * (inv * (1.f / kTop))};
+}
+// The same from top = max |y|, any. Rows so small that the reciprocal would overflow are scaled
+// up first (exactly). A subnormal scale has few bits: it is rounded up, so that no level passes
+// the top one, and the levels are those of the scale as it is then.
+template <int OUT>
+__device__ __forceinline__ Levels far_levels(float top, float rstd) {
+  constexpr float kTop = kTopLevel<OUT>;
+  const float up = top < kTiny ? kUp : 1.f;
+  Levels l{top / kTop, rstd * up, 0.f, 0.f};
+  float over = kTop, under = top * up;
   if (l.scale < 0x1p-126f) {
     if (l.scale * kTop < top) l.scale = __uint_as_float(__float_as_uint(l.scale) + 1u);
     over = 1.f, under = l.scale * kUp;
@@ -283,7 +295,7 @@ __global__ __launch_bounds__((TPR < 256 ? 256 : TPR)) void rmsnorm_fwd_kernel(
   Levels to{};
   if constexpr (kQuant) {
     const float top = m * rstd;
-    to = row_levels<OUT>(top);
+    to = row_levels<OUT>(m, top);
     if (far_row(m, top)) {  // (the same in all threads of a row, and so of a workgroup with barriers)
       float unused = 0.f, far = 0.f;
 #pragma unroll
@@ -296,10 +308,11 @@ __global__ __launch_bounds__((TPR < 256 ? 256 : TPR)) void rmsnorm_fwd_kernel(
       }
       if constexpr (TPR > 64) __syncthreads();  // red has been read
       row_reduce<TPR>(unused, far, red);
-      to = far_levels<OUT>(top == top ? far : top);
+      to = far_levels<OUT>(top == top ? far : top, rstd);
     }
     if (i0 == 0) q_scale[t] = to.scale;
   }
+  const float first = kQuant ? to.first : rstd;
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
     const int at = (i0 + v * TPR) * kN, left = d - at;
@@ -308,10 +321,9 @@ __global__ __launch_bounds__((TPR < 256 ? 256 : TPR)) void rmsnorm_fwd_kernel(
     repack(wt);
     float f[kN];
 #pragma unroll
-    for (int j = 0; j < kN; ++j) f[j] = elem(hv[v], j) * rstd * elem(wt, j);
+    for (int j = 0; j < kN; ++j) f[j] = elem(hv[v], j) * first * elem(wt, j);
     if constexpr (kQuant) {
-#pragma unroll
-      for (int j = 0; j < kN; ++j) f[j] = f[j] * to.up * to.inv;
+      to.apply(f);
       store_levels<OUT>(static_cast<uint8_t*>(y) + row + at, left, f);
     } else if (left > 0) {
       store_vec(static_cast<E*>(y) + row + at, left, hold<E>(f));
@@ -359,7 +371,7 @@ __global__ __launch_bounds__(kLoop) void rmsnorm_fwd_loop_kernel(int64_t T, int 
   Levels to{};
   if constexpr (kQuant) {
     const float top = m * rstd;
-    to = row_levels<OUT>(top);
+    to = row_levels<OUT>(m, top);
     if (far_row(m, top)) {
       float unused = 0.f, far = 0.f;
       for (int at = threadIdx.x * kN; at < d; at += kLoop * kN) {
@@ -369,19 +381,19 @@ __global__ __launch_bounds__(kLoop) void rmsnorm_fwd_loop_kernel(int64_t T, int 
       }
       __syncthreads();  // red has been read
       row_reduce<kLoop>(unused, far, red);
-      to = far_levels<OUT>(top == top ? far : top);
+      to = far_levels<OUT>(top == top ? far : top, rstd);
     }
   }
+  const float first = kQuant ? to.first : rstd;
   for (int at = threadIdx.x * kN; at < d; at += kLoop * kN) {
     const int left = d - at;
     const Held<E> v = h_at(at), wt = load_vec(w + at, left);
     if (res != nullptr) store_vec(h + row + at, left, v);
     float f[kN];
 #pragma unroll
-    for (int j = 0; j < kN; ++j) f[j] = elem(v, j) * rstd * elem(wt, j);
+    for (int j = 0; j < kN; ++j) f[j] = elem(v, j) * first * elem(wt, j);
     if constexpr (kQuant) {
-#pragma unroll
-      for (int j = 0; j < kN; ++j) f[j] = f[j] * to.up * to.inv;
+      to.apply(f);
       store_levels<OUT>(static_cast<uint8_t*>(y) + row + at, left, f);
     } else {
       store_vec(static_cast<E*>(y) + row + at, left, hold<E>(f));

@@ -366,3 +366,27 @@ def test_norm_of_millions_of_rows(q, dtype):
     g, n, r = host(x) * host(w), host(h) * host(rstd)[:, None], host(rstd)[:, None]
     mag = r * (np.abs(g) + np.abs(n) * np.abs(g * n).mean(1, keepdims=True))
     assert np.all(np.abs(host(dx) - rx) <= HALF[dtype] * np.abs(rx) + F32(d) * mag)
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "i8"])
+@pytest.mark.parametrize("T,d", [(900, 96), (400, 304), (600, 1000), (149, 1992), (36, 6398), (18, 16384), (24, 20660)])
+def test_rmsnorm_fwd_quant_halves_go_to_even(q, T, d, fmt):
+    """bf16 rows: every level equals the nearest one to the exact quotient v = h w top /
+    max |h w|, a quotient in the middle of two levels the even one. h w is A 2^a and the divisor
+    M 2^m with A, M < 2^16, a middle k 2^e with k < 2^(b + 1), b <= 7; v / middle is a fraction
+    with a numerator or denominator of at most M k or 127 A, so a v that is no middle is
+    further from it than 1 / (M k) > 2^-24 2^b / k, half a float32 step: neither float64's
+    rounding nor the one to float32 moves it there, and a middle is exact in both."""
+    g = torch.Generator().manual_seed(T)
+    x, w = make(T, T, d), (1 + 0.2 * torch.randn(d, generator=g)).to(BF)
+    kind = torch.float8_e4m3fn if fmt == "e4m3" else torch.int8
+    lv, _, _ = q.rmsnorm_fwd_quant(x.cuda(), w.cuda(), qdtype=kind)
+    p = host(x) * host(w)
+    v = p * o.TOP[fmt] / np.abs(p).max(1, keepdims=True)
+    if fmt == "i8":
+        halves, want = np.abs(v - np.trunc(v)) == 0.5, np.rint(v)
+    else:
+        step = 2.0 ** (np.floor(np.log2(np.maximum(np.abs(v), 2.0 ** -6))) - 3)
+        halves, want = np.abs(v / step - np.trunc(v / step)) == 0.5, o.e4m3_values()[o.e4m3_encode(v.astype(np.float32))]
+    assert halves.any()
+    assert np.array_equal(host(lv), want.reshape(T, d))
