@@ -224,7 +224,8 @@ __device__ __forceinline__ Levels far_levels(float top, float rstd) {
 
 // ---- forward ---------------------------------------------------------------------------
 // 8192 x 4096 bf16 with residual 44 us, 6.1 TB/s; 1 x 4096 to E4M3 3 us, a launch and two
-// latencies.
+// latencies. (Times here are over three sets of rows in turn, more than the memory-side
+// cache holds where the sizes are large.)
 template <typename E, int OUT, int TPR, int NV>
 __global__ __launch_bounds__((TPR < 256 ? 256 : TPR)) void rmsnorm_fwd_kernel(
     int64_t T, int d, float eps, const E* __restrict__ x, const E* __restrict__ res, const E* __restrict__ w,
@@ -332,8 +333,8 @@ __global__ __launch_bounds__((TPR < 256 ? 256 : TPR)) void rmsnorm_fwd_kernel(
 }
 
 // Rows wider than the registers of a workgroup hold: the row is read twice, the second
-// time mostly from L2 (h is formed again from x and the residual). 512 x 40000 bf16 19 us,
-// 4.3 TB/s.
+// time mostly from L2 (h is formed again from x and the residual). 512 x 40000 bf16 20 us,
+// 4.2 TB/s.
 constexpr int kLoop = 1024;
 template <typename E, int OUT>
 __global__ __launch_bounds__(kLoop) void rmsnorm_fwd_loop_kernel(int64_t T, int d, float eps, const E* __restrict__ x,
@@ -512,7 +513,7 @@ __global__ __launch_bounds__(BLOCK) void rmsnorm_bwd_kernel(int64_t T, int d, co
   }
 }
 
-// Rows wider than the registers hold: read twice (512 x 40000 bf16 19 us, 6.5 TB/s).
+// Rows wider than the registers hold: read twice (512 x 40000 bf16 30 us, 4.1 TB/s).
 template <typename E>
 __global__ __launch_bounds__(kLoop) void rmsnorm_bwd_loop_kernel(int64_t T, int d, const E* __restrict__ dy,
                                                                  const E* __restrict__ dh,
@@ -548,7 +549,7 @@ __global__ __launch_bounds__(kLoop) void rmsnorm_bwd_loop_kernel(int64_t T, int 
 }
 
 // part[b][i] = sum of dy n over the rows b, b + blocks, ... of column i; one vector of
-// columns a thread. With the join 28 us for 512 x 65536 bf16.
+// columns a thread. With the join 25 us for 512 x 40000 bf16, 3.2 TB/s.
 template <typename E>
 __global__ __launch_bounds__(256) void rmsnorm_dw_part_kernel(int64_t T, int d, const E* __restrict__ dy,
                                                               const E* __restrict__ h,
@@ -608,8 +609,8 @@ __global__ __launch_bounds__(256) void zero_kernel(E* __restrict__ p, int64_t n)
 }
 
 // Threads and vectors a thread of a row of `vecs` vectors: up to two vectors a thread, from
-// one wave, 4 or 16, as long as 16 waves of two hold the row. Measured (bf16 forward with
-// residual, us): 8192 x 4096 at 256 threads of two 47, 1024 of one 49, 64 of eight 55; 1 x
+// one wave, 4 or 16, as long as 16 waves of two hold the row. Measured in one sweep of
+// launches back to back, each with its gap (bf16 forward with residual, us): 8192 x 4096 at 256 threads of two 47, 1024 of one 49, 64 of eight 55; 1 x
 // 4096 at 256 of two 2.9, 64 of eight 5.3; 8192 x 1024 at 64 of two 11.1, 256 of one 12.9;
 // but 400 x 1024 at 256 of one 2.9, 64 of two 4.2 (few rows leave the GPU idle whatever
 // is chosen, and one vector a thread has the shorter way from its loads to its stores).
@@ -651,9 +652,9 @@ hipError_t fwd(int64_t T, int d, float eps, const void* xv, const void* rv, cons
                float* q_scale, float* rstd, hipStream_t stream) {
   const auto x = static_cast<const E*>(xv), res = static_cast<const E*>(rv), w = static_cast<const E*>(wv);
   const auto h = static_cast<E*>(hv);
-  // Up to 32768 values of a row in registers (1 x 28672 float32 6.8 us, 2048 x 20000 99; the loop
-  // 9.9 and 119), but 16384 of bf16 rows with levels, whose arithmetic does not fit beside
-  // more of them (78 x 20856 8.1 us, 2048 x 20000 58; the loop 7.3 and 46).
+  // Up to 32768 values of a row in registers (1 x 28672 float32 5.3 us, 2048 x 20000 68, with the
+  // residual 129; the loop 7.4, 84 and 163), but 16384 of bf16 rows with levels, whose arithmetic
+  // does not fit beside more of them (78 x 20856 6.8 us, 2048 x 20000 48; the loop 5.9 and 34).
   constexpr int kMost = (Vec<E>::kN == 8 && (OUT == kRowE4m3 || OUT == kRowI8) ? 16 : 32) / Vec<E>::kN;
   const RowShape sh = row_shape(T, (d + Vec<E>::kN - 1) / Vec<E>::kN, kMost);
   if (sh.tpr == 0)
@@ -689,8 +690,9 @@ hipError_t bwd(int64_t T, int d, const void* dyv, const void* dhv, const void* h
   const auto dx = static_cast<E*>(dxv), dw = static_cast<E*>(dwv);
   const auto part = static_cast<float*>(workspace);
   // dw's sums take a register an element: 16 elements a thread leave four waves a SIMD. Wider
-  // rows are read twice, and have their dw in a pass of its own (2048 x 20000 without dw: 33
-  // us, in registers 42; float32 80 and 94; with the sums too they spill).
+  // rows are read twice, and have their dw in a pass of its own (78 x 20856 without dw 5.8 us,
+  // in registers 6.9; many rows about alike, 2048 x 20000 with dh 62 and 63, float32 126 and 129;
+  // with the sums too they spill).
   constexpr int kMost = 16 / Vec<E>::kN;
   const int64_t vecs = (d + Vec<E>::kN - 1) / Vec<E>::kN;
   const RowShape sh = row_shape(T, vecs, kMost);

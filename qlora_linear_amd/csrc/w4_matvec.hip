@@ -616,7 +616,7 @@ hipError_t run_shared(Call c) {
 }
 
 // Which kernel, and over how many workgroups d_in is split (their float32 sums meet in
-// the workspace and a second launch joins them, about 2 us). Measured (us):
+// the workspace and a second launch of 4 to 5 us joins them). Measured, it included (us):
 //   * up to 16 rows. Over 768 tiles there are workgroups enough: four tiles each (8192 ->
 //     28672 at 1 row 26; two tiles and 16 waves 32). Fewer tiles at a usual depth: two tiles
 //     over 16 waves (4096 -> 6144 at 4 rows 5.9; one tile 6.9), one tile below 257 (4096 ->

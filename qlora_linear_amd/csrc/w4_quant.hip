@@ -66,7 +66,8 @@ __device__ __forceinline__ void group_extrema(int group, float& lo, float& hi) {
 
 // One 256-thread workgroup per tile. Thread t: row t >> 4, columns 8 (t & 15) .. + 7,
 // so a group is G / 8 consecutive lanes. Bound by its arithmetic rather than by HBM
-// (about 14 instructions an element): no division as a rule, the codes put together as
+// (27 vector instructions an element by the counter, which keep the vector units busy all of
+// the time, 13.6 us of 4-cycle issues at 2 GHz): no division as a rule, the codes put together as
 // floats (sums of multiples of powers of 16 below 2^16 are exact), two conversions a word.
 // 4096 x 4096 bf16 13.8 us, 3.1 TB/s.
 template <typename In>
