@@ -36,7 +36,8 @@ typedef enum { LN_E4M3 = 2, LN_I8 = 3 } ln_qtype;
  * rmsnorm_fwd — the norm of T rows of d values, with the residual's addition:
  *     h = x + residual      (the float32 sum rounded to dtype; h = x without a residual)
  *     y = h rstd w,   rstd = 1 / sqrt(mean(h^2) + eps)        per row
- * The sum of squares runs over the rounded h in float32; y is rounded once.
+ * The sum of squares runs over the rounded h in float32 (where it overflows, |h| above 1e19 /
+ * sqrt(d), rstd is 0); y is rounded once.
  *   dtype     LN_BF16 or LN_F32, of x, residual, w, h and y
  *   eps       > 0, finite
  *   x, residual, h, y   [T, d]; residual and h both given or both NULL

@@ -185,7 +185,7 @@ __device__ __forceinline__ int64_t row_block() { return static_cast<int64_t>(blo
 // as that and goes to the even one.
 // h w may leave float32's normal range where y does not: near its ends (and in rows of zeros)
 // the largest y is found again, from y, and levels are y times a reciprocal of it.
-constexpr float kTiny = 0x1p-100f, kUp = 0x1p64f, kHuge = 0x1p127f;
+constexpr float kTiny = 0x1p-100f, kUp = 0x1p48f, kHuge = 0x1p127f;
 __device__ __forceinline__ bool far_row(float m, float top) {
   return __builtin_expect(!(fminf(m, top) >= kTiny && top <= kHuge), 0);
 }
@@ -206,7 +206,7 @@ __device__ __forceinline__ Levels row_levels(float m, float top) {
   return Levels{top / kTop, 1.f, inv, __builtin_fmaf(-inv, m, kTop) * (inv * (1.f / kTop))};
 }
 // The same from top = max |y|, any. Rows so small that the reciprocal would overflow are scaled
-// up first (exactly). A subnormal scale has few bits: it is rounded up, so that no level passes
+// up first (exactly; rstd, at most 2^75 for the least eps, does not overflow by it). A subnormal scale has few bits: it is rounded up, so that no level passes
 // the top one, and the levels are those of the scale as it is then.
 template <int OUT>
 __device__ __forceinline__ Levels far_levels(float top, float rstd) {

@@ -83,7 +83,8 @@ def F32(d):
 # sizes of x's and w's values, and eps
 FAR = {"product-underflows": (1e-24, 1e-20, 1e-5), "scale-subnormal": (1.0, 1e-37, 1e-5),
        "scale-of-few-bits": (1.0, 3e-40, 1e-5), "all-below-float32": (1e-30, 1e-25, 1e-5),
-       "product-overflows": (1e16, 1e23, 1e-5), "rows-far-below-eps": (1e-24, 1e-20, 1e-37)}
+       "product-overflows": (1e16, 1e23, 1e-5), "rows-far-below-eps": (1e-24, 1e-20, 1e-37),
+       "least-eps": (1e-27, 1e-20, 1.4e-45)}
 
 
 @pytest.mark.parametrize("fmt", ["e4m3", "i8"])
@@ -390,3 +391,31 @@ def test_rmsnorm_fwd_quant_halves_go_to_even(q, T, d, fmt):
         halves, want = np.abs(v / step - np.trunc(v / step)) == 0.5, o.e4m3_values()[o.e4m3_encode(v.astype(np.float32))]
     assert halves.any()
     assert np.array_equal(host(lv), want.reshape(T, d))
+
+
+@pytest.mark.parametrize("kind", [BF, torch.float8_e4m3fn, torch.int8], ids=["bf16", "e4m3", "i8"])
+@pytest.mark.parametrize("T", [1, 16, 20, 64])
+def test_w4_matvec_widest(q, T, kind):
+    """2^22 columns. x is zero but for one column in a thousand and the last ones: sums of at most
+    4300 products below 2^7, multiples of 1/4: exact."""
+    K, N, group = 1 << 22, 19, 128
+    g = torch.Generator().manual_seed(T)
+    x = torch.zeros(T, K)
+    x[:, ::997] = torch.randint(-1, 2, (T, -(-K // 997)), generator=g).float()
+    x[:, -3:] = 1
+    codes = torch.randint(0, 256, (2, K // 128, 1024), generator=g, dtype=torch.uint8).cuda()
+    scales = (2.0 ** torch.randint(-2, 2, (2, K // group, 16), generator=g)).to(BF).cuda()
+    W = q.w4_dequantize(codes, scales, d_out=N, d_in=K, dtype=F)
+    on = np.flatnonzero((x != 0).any(0).numpy())
+    want = host(x)[:, on] @ host(W)[:, on].T
+    y = q.w4_matvec(x.to(kind).cuda(), codes, scales, d_out=N, dtype=F, group=group)
+    assert np.array_equal(host(y), want)
+
+
+@pytest.mark.parametrize("kind", [BF, torch.int8], ids=["bf16", "i8"])
+def test_w4_matvec_most_rows(q, kind):
+    x, packs, want = exact_case(q, 1, 4096, 64, (17,), 32, True, kind)
+    y = q.w4_matvec(x.repeat(512, 1), *packs[0], d_out=17, dtype=F, group=32)
+    assert np.array_equal(host(y[:4096]), want[0]) and torch.equal(y, y[:4096].repeat(512, 1))
+    with pytest.raises(q.LoraNF4Error):
+        q.w4_matvec(x.repeat(513, 1), *packs[0], d_out=17, group=32)
