@@ -419,3 +419,21 @@ def test_w4_matvec_most_rows(q, kind):
     assert np.array_equal(host(y[:4096]), want[0]) and torch.equal(y, y[:4096].repeat(512, 1))
     with pytest.raises(q.LoraNF4Error):
         q.w4_matvec(x.repeat(513, 1), *packs[0], d_out=17, group=32)
+
+
+@pytest.mark.parametrize("zero_points", [False, True])
+@pytest.mark.parametrize("size", [2.0 ** 126, 1e30, 1e-30, 1e-36, 1e-38, 1e-40, 1e-43, 3e-45])
+def test_w4_quantize_far_values(q, size, zero_points):
+    """float32 weights up to the largest ranges and down to subnormal scales, bit for bit."""
+    g = torch.Generator().manual_seed(3)
+    w = ((torch.rand(40, 256, generator=g, dtype=torch.float64) * 2 - 1) * size).float()
+    w[3, 64:128] = 0
+    for group in (32, 128):
+        codes, scales, zeros = q.w4_quantize(w.cuda(), group, zero_points)
+        c, s, z = o.w4_quantize(w.numpy(), group, zero_points)
+        pc, ps, pz = o.w4_pack(c, s, z)
+        assert np.array_equal(scales.float().cpu().numpy(), ps)
+        assert np.array_equal(codes.cpu().numpy(), pc)
+        assert not zero_points or np.array_equal(zeros.cpu().numpy(), pz)
+        assert np.array_equal(host(q.w4_dequantize(codes, scales, zeros, d_out=40, d_in=256, dtype=F)),
+                              o.w4_values(c, s, z, group).astype(np.float32))
