@@ -20,7 +20,8 @@ library has not been built, the first call raises.
     alpha_rs = rslora_alpha(lora_alpha, r)                       # scale alpha / sqrt(r)
 
 The RMS norm before the linear and the 4-bit group-scaled product that serves a merged
-weight (C ABI in include/norm_w4.h) are in the submodule norm_w4 and exported here too.
+weight (C ABI in include/norm_w4.h) are in the submodule norm_w4 and exported here too, and so
+is the paged 4-bit cache of keys and values with its attention (include/kv4.h) from kv4.
 """
 from __future__ import annotations
 
@@ -542,3 +543,8 @@ from .norm_w4 import *  # noqa: E402,F401,F403  (registers its entry points with
 from . import norm_w4 as _norm_w4  # noqa: E402
 
 __all__ += _norm_w4.__all__
+
+from .kv4 import *  # noqa: E402,F401,F403  (as above)
+from . import kv4 as _kv4  # noqa: E402
+
+__all__ += _kv4.__all__
