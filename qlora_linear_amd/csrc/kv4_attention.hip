@@ -34,7 +34,22 @@ constexpr int kThreads = 256;
 constexpr int kWaves = 4;
 constexpr int kTile = 32;             // keys of a wave's tile
 constexpr float kLowest = -3.0e38f;   // the maximum of no keys
-constexpr int kListed = 1024;         // sequences whose steps are summed in LDS
+constexpr int kListed = 512;         // sequences whose steps are summed in LDS
+
+// 16-row tiles of a row block at most, and the waves a SIMD that the registers are cut for
+// (workgroups a CU, then): as many as need no scratch memory.
+constexpr int most_nq(int D) { return D == 64 ? 4 : D == 128 ? 2 : 1; }
+constexpr int waves_of(int D, int G, int NQ) {
+  if (D == 64) return NQ == 1 ? 4 : NQ == 2 && G == 64 ? 3 : 2;
+  return D == 128 && NQ == 1 && G >= 64 ? 3 : 2;
+}
+
+// A value that all lanes share, as one scalar.
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+// Memory that no kernel of the call writes: a read at a shared place is a scalar one, and is not
+// counted with the loads of codes.
+typedef const __attribute__((address_space(4))) int32_t* Const;
 
 struct Plan {
   int wgs;           // workgroups that share the steps
@@ -79,8 +94,9 @@ __device__ __forceinline__ void seq_rows(const Kv4Attention& a, int b, int& c0, 
   if (a.cu_q == nullptr) {
     c0 = b, n = 1;
   } else {
-    c0 = min(max(a.cu_q[b], 0), a.T);
-    n = min(max(a.cu_q[b + 1], c0), a.T) - c0;
+    const Const cu = (Const)a.cu_q;
+    c0 = min(max(cu[b], 0), a.T);
+    n = min(max(cu[b + 1], c0), a.T) - c0;
   }
 }
 
@@ -88,7 +104,7 @@ __device__ __forceinline__ Block make_block(const Args& g, int b, int rb) {
   Block k;
   k.b = b;
   seq_rows(g.a, b, k.c0, k.n);
-  k.len = min(max(g.a.lens[b], 0), g.a.max_pages * g.c.page_size);
+  k.len = min(max(((Const)g.a.lens)[b], 0), g.a.max_pages * g.c.page_size);
   k.row0 = rb * g.rows;
   k.rows = min(g.rows, k.n * g.heads - k.row0);
   const int j0 = k.row0 / g.heads, j1 = (k.row0 + max(k.rows, 1) - 1) / g.heads;
@@ -191,30 +207,41 @@ __device__ __forceinline__ uint4 wide_codes(uint32_t lo, uint32_t hi) {
                two(hi, std::true_type{})};
 }
 
+// The steps and least values of a wave's tile, in LDS: they come as one word a lane and are read
+// as four keys', so that registers hold them only while they are used.
+template <int NG>
+struct Scales {
+  uint32_t k[NG][kTile], v[NG][kTile];
+};
+
 template <int D, int G, int NQ>
 struct Wave {
   static constexpr int C = D / 32, NG = D / G, CG = G / 32;
+  static constexpr int NP = NG < 2 ? 1 : NG / 2;  // words of scales a lane loads
+  static constexpr bool kShared = NQ > 2;         // the queries' operands in LDS, for all waves
 
   struct alignas(D / 8 < 16 ? D / 8 : 16) Words {
     uint32_t w[C];
   };
-  // a tile's codes and parameters as they lie in memory
+  // A tile's codes and scales, of keys or of values. With one group a row the word of scales that
+  // comes with the keys is a key's in the lower lanes and a value's in the upper ones.
   struct Raw {
-    Words k[2], v[2];
-    uint4 ks[2][NG], vs[2][NG];
+    Words w[2];
+    uint32_t p[NP];
   };
 
-  uint4 q[NQ][C];
-  float q_sum[NQ][NG];  // sum of a query's group, in its lanes
+  uint4 q[kShared ? 1 : NQ][C];
+  uint4 (*shared)[C][64];
+  Scales<NG>* scales;
+  float q_sum[NQ][NG];      // sum of a query's group, in its lanes
   int first[NQ], last[NQ];  // the keys [first, last) that the lane's query sees
   int all_lo, all_hi;       // the keys that every row sees
-  int tiles_q;              // tiles that hold rows
   f32x4_t o[NQ][C][2], z[NQ][NG];
   float mid[NQ][NG], m[NQ], l[NQ];
+  float x[NQ][2][4];        // a tile's scores
 
-  __device__ __forceinline__ void begin(const Args& g, const Block& k, int h) {
+  __device__ __forceinline__ void begin(const Args& g, const Block& k, int h, int wave) {
     const int lane = threadIdx.x & 63, col = lane & 15, seg = lane >> 4;
-    tiles_q = max(1, (k.rows + 15) / 16);
     // every row sees what the first does, from where the last one's window begins
     all_hi = max(k.len - k.n + k.row0 / g.heads + 1, 0);
     all_lo = g.a.window > 0 ? max(k.len - k.n + (k.row0 + max(k.rows, 1) - 1) / g.heads + 1 - g.a.window, 0) : 0;
@@ -227,13 +254,18 @@ struct Wave {
       first[t] = g.a.window > 0 ? max(last[t] - g.a.window, 0) : 0;
       const uint16_t* from = g.a.q + (k.c0 + j) * g.a.q_stride + (h * g.heads + row - j * g.heads) * D + 8 * seg;
       const bool ok = 16 * t + col < k.rows;
+      uint4(&mine)[C] = q[kShared ? 0 : t];
 #pragma unroll
-      for (int c = 0; c < C; ++c) q[t][c] = ok ? *reinterpret_cast<const uint4*>(from + 32 * c) : uint4{0, 0, 0, 0};
+      for (int c = 0; c < C; ++c) mine[c] = ok ? *reinterpret_cast<const uint4*>(from + 32 * c) : uint4{0, 0, 0, 0};
+      if (kShared && t % kWaves == wave) {
+#pragma unroll
+        for (int c = 0; c < C; ++c) shared[t][c][lane] = mine[c];
+      }
 #pragma unroll
       for (int i = 0; i < NG; ++i) {
         f32x4_t s = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int c = i * CG; c < (i + 1) * CG; ++c) s = mfma16(ones, q[t][c], s);
+        for (int c = i * CG; c < (i + 1) * CG; ++c) s = mfma16(ones, mine[c], s);
         q_sum[t][i] = s[0];
         z[t][i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
         mid[t][i] = 0.f;
@@ -245,80 +277,116 @@ struct Wave {
     }
   }
 
-  static __device__ __forceinline__ void load(const Args& g, int page, int tile_in_page, int h, Raw& r) {
+  // row: the tile's first token in its page and head, counted over all pages and heads; par: the
+  // same of its scales.
+  static __device__ __forceinline__ void load_keys(const Args& g, int64_t row, int64_t par, Raw& r) {
     const int lane = threadIdx.x & 63, col = lane & 15, seg = lane >> 4;
-    const int64_t ph = static_cast<int64_t>(page) * g.c.n_kv + h;
-    const int tok = tile_in_page * kTile;
-    const int64_t codes = (ph * g.c.page_size + tok) * (D / 2);
-    const uint8_t* kc = g.c.k_codes + codes + col * (D / 2) + seg * (D / 8);
-    const uint8_t* vc = g.c.v_codes + codes + seg * (2 * D) + col * (D / 8);
-    const int64_t par = (ph * NG * g.c.page_size + tok + 4 * seg) * 2;
-    const uint16_t *ks = g.c.k_scales + par, *vs = g.c.v_scales + par;
+    load_codes(g.c.k_codes + row * (D / 2), col * (D / 2) + seg * (D / 8), 16 * (D / 2), r);
+    load_scales(NG == 1 && lane >= kTile ? g.c.v_scales : g.c.k_scales, par, g.c.page_size, r);
+  }
+  static __device__ __forceinline__ void load_values(const Args& g, int64_t row, int64_t par, Raw& r) {
+    const int lane = threadIdx.x & 63, col = lane & 15, seg = lane >> 4;
+    load_codes(g.c.v_codes + row * (D / 2), seg * (2 * D) + col * (D / 8), 8 * D, r);
+    if constexpr (NG > 1) load_scales(g.c.v_scales, par, g.c.page_size, r);
+  }
+  static __device__ __forceinline__ void load_codes(const uint8_t* codes, int at, int half, Raw& r) {
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      r.k[s] = *reinterpret_cast<const Words*>(kc + s * 16 * (D / 2));
-      r.v[s] = *reinterpret_cast<const Words*>(vc + s * 8 * D);
+    for (int s = 0; s < 2; ++s) r.w[s] = *reinterpret_cast<const Words*>(codes + s * half + at);
+  }
+  static __device__ __forceinline__ void load_scales(const uint16_t* scales, int64_t par, int page_size, Raw& r) {
+    const int lane = threadIdx.x & 63;
+    const uint32_t* from = reinterpret_cast<const uint32_t*>(scales) + par + lane % kTile;
+    if constexpr (NG == 1) {
+      r.p[0] = *from;
+    } else {
 #pragma unroll
-      for (int i = 0; i < NG; ++i) {
-        r.ks[s][i] = *reinterpret_cast<const uint4*>(ks + (i * g.c.page_size + 16 * s) * 2);
-        r.vs[s][i] = *reinterpret_cast<const uint4*>(vs + (i * g.c.page_size + 16 * s) * 2);
-      }
+      for (int i = 0; i < NP; ++i) r.p[i] = from[(2 * i + lane / kTile) * page_size];
+    }
+  }
+  // Scales of values that no row sees may be no numbers: keys outside [lo, hi) get zeros.
+  __device__ __forceinline__ void put_key_scales(const Raw& r, int key0, int lo, int hi) {
+    const int lane = threadIdx.x & 63;
+    if constexpr (NG == 1) {
+      const int key = key0 + lane % kTile;
+      (&scales->k[0][0])[lane] = lane >= kTile && (key < lo || key >= hi) ? 0u : r.p[0];
+    } else {
+#pragma unroll
+      for (int i = 0; i < NP; ++i) (&scales->k[0][0])[64 * i + lane] = r.p[i];
+    }
+  }
+  __device__ __forceinline__ void put_value_scales(const Raw& r, int key0, int lo, int hi) {
+    if constexpr (NG > 1) {
+      const int lane = threadIdx.x & 63, key = key0 + lane % kTile;
+#pragma unroll
+      for (int i = 0; i < NP; ++i) (&scales->v[0][0])[64 * i + lane] = key < lo || key >= hi ? 0u : r.p[i];
     }
   }
 
-  static __device__ __forceinline__ float step(const uint4& p, int i) {
-    const uint32_t w = i == 0 ? p.x : i == 1 ? p.y : i == 2 ? p.z : p.w;
-    return __uint_as_float(w << 16);
-  }
-  static __device__ __forceinline__ float least(const uint4& p, int i) {
-    const uint32_t w = i == 0 ? p.x : i == 1 ? p.y : i == 2 ? p.z : p.w;
-    return __uint_as_float(w & 0xFFFF0000u);
+  // Steps and least values of four keys.
+  static __device__ __forceinline__ void split(const uint32_t* from, float (&s)[4], float (&least)[4]) {
+    const uint4 p = *reinterpret_cast<const uint4*>(from);
+    const uint32_t w[4] = {p.x, p.y, p.z, p.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) s[e] = __uint_as_float(w[e] << 16), least[e] = __uint_as_float(w[e] & 0xFFFF0000u);
   }
 
-  // One tile: keys key0 .. key0 + 31. MASK: some row does not see some of them.
-  template <bool MASK>
-  __device__ __forceinline__ void tile(const Raw& r, int key0, float scale2) {
-    const int seg = (threadIdx.x & 63) >> 4;
-    float x[NQ][2][4];
+  // The scores of a tile's keys, of NT tiles of queries.
+  template <int NT>
+  __device__ __forceinline__ void score(const Raw& r) {
+    const int lane = threadIdx.x & 63, seg = lane >> 4;
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
 #pragma unroll
       for (int i = 0; i < NG; ++i) {
-        f32x4_t acc[NQ];
+        f32x4_t acc[NT];
 #pragma unroll
-        for (int t = 0; t < NQ; ++t) acc[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+        for (int t = 0; t < NT; ++t) acc[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int c = i * CG; c < (i + 1) * CG; ++c) {
-          const uint32_t w = r.k[s].w[c];
+          const uint32_t w = r.w[s].w[c];
           const uint4 wide = wide_codes(w & 0x0F0F0F0Fu, (w >> 4) & 0x0F0F0F0Fu);
 #pragma unroll
-          for (int t = 0; t < NQ; ++t)
-            if (NQ == 1 || t < tiles_q) acc[t] = mfma16(wide, q[t][c], acc[t]);
+          for (int t = 0; t < NT; ++t) acc[t] = mfma16(wide, kShared ? shared[t][c][lane] : q[kShared ? 0 : t][c], acc[t]);
         }
+        float step[4], least[4];
+        split(&scales->k[i][16 * s + 4 * seg], step, least);
 #pragma unroll
-        for (int t = 0; t < NQ; ++t)
-          if (NQ == 1 || t < tiles_q) {
+        for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float b = least(r.ks[s][i], e) * q_sum[t][i];
-              x[t][s][e] = __builtin_fmaf(step(r.ks[s][i], e), acc[t][e], i == 0 ? b : x[t][s][e] + b);
-            }
+          for (int e = 0; e < 4; ++e) {
+            const float b = i == 0 ? least[e] * q_sum[t][i] : __builtin_fmaf(least[e], q_sum[t][i], x[t][s][e]);
+            x[t][s][e] = __builtin_fmaf(step[e], acc[t][e], b);
           }
       }
     }
-    uint4 p[NQ][NG];
+    // Nothing that reads the keys comes after this and no load before (else the next keys are
+    // loaded into other registers, and moves at the tile's end wait for them).
 #pragma unroll
-    for (int t = 0; t < NQ; ++t) {
-      if (NQ > 1 && t >= tiles_q) continue;
-      if constexpr (MASK) {
+    for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int s = 0; s < 2; ++s)
+      for (int s = 0; s < 2; ++s)
+        asm volatile("" : "+v"(x[t][s][0]), "+v"(x[t][s][1]), "+v"(x[t][s][2]), "+v"(x[t][s][3]) : : "memory");
+  }
+
+  // Some row does not see some of the keys key0 .. key0 + 31, and no row those below lo.
+  template <int NT>
+  __device__ __forceinline__ void hide(int key0, int lo) {
+    const int seg = (threadIdx.x & 63) >> 4;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int key = key0 + 16 * s + 4 * seg + e;
-            if (key < first[t] || key >= last[t]) x[t][s][e] = -__builtin_inff();
-          }
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int key = key0 + 16 * (e >> 2) + 4 * seg + (e & 3);
+        if (key < max(first[t], lo) || key >= last[t]) x[t][e >> 2][e & 3] = -__builtin_inff();
       }
+  }
+
+  // The tile's part of the sums.
+  template <int NT>
+  __device__ __forceinline__ void sum(const Raw& r, float scale2) {
+    const int seg = (threadIdx.x & 63) >> 4;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
       float top = x[t][0][0];
 #pragma unroll
       for (int e = 1; e < 8; ++e) top = fmaxf(top, x[t][e >> 2][e & 3]);
@@ -346,46 +414,99 @@ struct Wave {
         v = __builtin_amdgcn_exp2f(__builtin_fmaf(v, scale2, -m[t]));
         l[t] += v;
       }
-#pragma unroll
-      for (int i = 0; i < NG; ++i) {
-        float w[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float v = x[t][e >> 2][e & 3], s = step(r.vs[e >> 2][i], e & 3);
-          const float centre = __builtin_fmaf(8.f, s, least(r.vs[e >> 2][i], e & 3));
-          // (what a masked place holds may be no number)
-          w[e] = MASK && v == 0.f ? 0.f : v * s;
-          mid[t][i] = MASK && v == 0.f ? mid[t][i] : __builtin_fmaf(v, centre, mid[t][i]);
-        }
-        p[t][i] = uint4{pack_bf16x2(w[0], w[1]), pack_bf16x2(w[2], w[3]), pack_bf16x2(w[4], w[5]),
-                        pack_bf16x2(w[6], w[7])};
-      }
     }
     const uint4 ones = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
 #pragma unroll
     for (int i = 0; i < NG; ++i) {
+      float step[2][4], centre[2][4];
 #pragma unroll
-      for (int t = 0; t < NQ; ++t)
-        if (NQ == 1 || t < tiles_q) z[t][i] = mfma16(ones, p[t][i], z[t][i]);
+      for (int s = 0; s < 2; ++s) {
+        split(&scales->v[i][16 * s + 4 * seg], step[s], centre[s]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) centre[s][e] = __builtin_fmaf(8.f, step[s][e], centre[s][e]);
+      }
+      uint4 p[NT];
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        float w[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float v = x[t][e >> 2][e & 3];
+          w[e] = v * step[e >> 2][e & 3];
+          mid[t][i] = __builtin_fmaf(v, centre[e >> 2][e & 3], mid[t][i]);
+        }
+        p[t] = uint4{pack_bf16x2(w[0], w[1]), pack_bf16x2(w[2], w[3]), pack_bf16x2(w[4], w[5]), pack_bf16x2(w[6], w[7])};
+        z[t][i] = mfma16(ones, p[t], z[t][i]);
+      }
 #pragma unroll
       for (int c = i * CG; c < (i + 1) * CG; ++c) {
+        // Products come in this order (an empty statement, no instruction: else every code is
+        // widened ahead of all of them, into registers that more waves need)
+        uint32_t w0 = r.w[0].w[c], w1 = r.w[1].w[c];
+        if (c == 0) {
+          asm volatile("" : "+v"(w0), "+v"(w1));
+        } else if constexpr (NT == 1) {
+          asm volatile("" : "+v"(w0), "+v"(w1), "+v"(o[0][c - 1][0]), "+v"(o[0][c - 1][1]));
+        } else {
+#pragma unroll
+          for (int t = 0; t < NT; ++t) asm volatile("" : "+v"(w0), "+v"(w1), "+v"(o[t][c - 1][0]), "+v"(o[t][c - 1][1]));
+        }
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-          const uint4 a = wide_codes((r.v[0].w[c] >> (4 * half)) & 0x0F0F0F0Fu, (r.v[1].w[c] >> (4 * half)) & 0x0F0F0F0Fu);
-          // the conversion's two words of a tile's four keys are operands 0 .. 3 and 4 .. 7
+          const uint4 a = wide_codes((w0 >> (4 * half)) & 0x0F0F0F0Fu, (w1 >> (4 * half)) & 0x0F0F0F0Fu);
 #pragma unroll
-          for (int t = 0; t < NQ; ++t)
-            if (NQ == 1 || t < tiles_q) o[t][c][half] = mfma16(a, p[t][i], o[t][c][half]);
+          for (int t = 0; t < NT; ++t) o[t][c][half] = mfma16(a, p[t], o[t][c][half]);
         }
       }
     }
+  }
+
+  // The wave's tiles t, t + 4, .. below t_end of a key head. A tile's keys are loaded while the
+  // values of the one before are multiplied, its values while its keys are, each into the registers
+  // that were just read.
+  template <int NT>
+  __device__ __forceinline__ void tiles(const Args& g, const Block& k, int h, int t, int t_end) {
+    const Const table = (Const)(g.a.block_table + static_cast<int64_t>(k.b) * g.a.max_pages);
+    auto slot_of = [&](int t) { return g.tiles_per_page == 1 ? t : static_cast<int>(__umulhi(t, g.page_inv)); };
+    // a tile's place in the cache; of a page that does not exist page 0, with its keys hidden
+    int64_t row, par;
+    bool gone;
+    auto place = [&](int t, int slot, int page) {
+      gone = page < 0 || page >= g.c.n_pages;
+      const int64_t ph = static_cast<int64_t>(gone ? 0 : page) * g.c.n_kv + h;
+      const int tok = (t - slot * g.tiles_per_page) * kTile;
+      row = ph * g.c.page_size + tok;
+      par = ph * NG * g.c.page_size + tok;
+    };
+    Raw keys, values;
+    const int slot = slot_of(t);
+    place(t, slot, table[slot]);
+    load_keys(g, row, par, keys);
+    load_values(g, row, par, values);
+    int next_slot = slot_of(min(t + kWaves, t_end - 1)), page = table[next_slot];
+    bool more;
+    do {
+      const int key0 = t * kTile, lo = gone ? key0 + kTile : k.lo;
+      const bool border = gone || key0 < all_lo || key0 + kTile > all_hi;
+      t += kWaves;
+      more = t < t_end;
+      put_key_scales(keys, key0, lo, k.hi);
+      score<NT>(keys);
+      if (more) place(t, next_slot, page);  // (the last tile is loaded again: counted waits need no two ways)
+      load_keys(g, row, par, keys);
+      next_slot = slot_of(min(t + kWaves, t_end - 1));
+      page = table[next_slot];
+      if (border) hide<NT>(key0, lo);
+      put_value_scales(values, key0, lo, k.hi);
+      sum<NT>(values, g.scale2);
+      load_values(g, row, par, values);
+    } while (more);
   }
 
   // The sums over the wave's lanes, centres applied: o holds sum p v of the tiles so far.
   __device__ __forceinline__ void finish() {
 #pragma unroll
     for (int t = 0; t < NQ; ++t) {
-      if (NQ > 1 && t >= tiles_q) continue;
       l[t] += __shfl_xor(l[t], 16);
       l[t] += __shfl_xor(l[t], 32);
 #pragma unroll
@@ -415,12 +536,18 @@ __device__ __forceinline__ void store4(uint16_t* p, float a, float b, float c, f
 }
 
 template <int D, int G, int NQ>
-__global__ __launch_bounds__(kThreads) void kv4_attention_kernel(Args g) {
+__global__ __launch_bounds__(kThreads, waves_of(D, G, NQ)) void kv4_attention_kernel(Args g) {
+  typedef Wave<D, G, NQ> W;
   constexpr int C = D / 32;
-  __shared__ Joined<D> joined;
+  __shared__ union {
+    Joined<D> joined;
+    uint4 q[W::kShared ? NQ : 1][C][64];
+  } space;
+  Joined<D>& joined = space.joined;
+  __shared__ Scales<W::NG> scales[kWaves];
   __shared__ int listed[kListed + 1];
   __shared__ int part[kWaves];
-  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
+  const int tid = threadIdx.x, wave = uniform(tid >> 6), lane = tid & 63;
   const int n_kv = g.c.n_kv;
 
   // the steps before every row block
@@ -453,31 +580,31 @@ __global__ __launch_bounds__(kThreads) void kv4_attention_kernel(Args g) {
 
   Cut cut = {0, 0, 0, 0, 0};
   int64_t at = begin;
-  int item = __builtin_amdgcn_readfirstlane(place_of(before, items, at, n_kv));
+  int item = uniform(place_of(before, items, at, n_kv));
   while (at < end) {
-    const int base = __builtin_amdgcn_readfirstlane(before[item]);
-    const int own = __builtin_amdgcn_readfirstlane(before[item + 1]) - base;  // steps of the row block
+    const int base = uniform(before[item]);
+    const int own = uniform(before[item + 1]) - base;  // steps of the row block
     const int64_t in = at - static_cast<int64_t>(base) * n_kv;
-    const int h = static_cast<int>(in / own);
-    const int s0 = static_cast<int>(in - static_cast<int64_t>(h) * own);
-    const int s1 = static_cast<int>(min(static_cast<int64_t>(own), s0 + end - at));
-    const int b = g.per_sequence ? item : __builtin_amdgcn_readfirstlane(g.seq[item]);
-    const Block k = make_block(g, b, g.per_sequence ? 0 : item - __builtin_amdgcn_readfirstlane(g.first[b]));
+    const int h = uniform(static_cast<int>(in / own));
+    const int s0 = uniform(static_cast<int>(in - static_cast<int64_t>(h) * own));
+    const int s1 = uniform(static_cast<int>(min(static_cast<int64_t>(own), s0 + end - at)));
+    const int b = g.per_sequence ? item : uniform(g.seq[item]);
+    Block k = make_block(g, b, g.per_sequence ? 0 : item - uniform(g.first[b]));
+    k.c0 = uniform(k.c0), k.n = uniform(k.n), k.len = uniform(k.len), k.row0 = uniform(k.row0);
+    k.rows = uniform(k.rows), k.lo = uniform(k.lo), k.hi = uniform(k.hi);
 
     Wave<D, G, NQ> w;
-    w.begin(g, k, h);
-    const int t_end = (k.hi + kTile - 1) / kTile;
-    const int32_t* table = g.a.block_table + static_cast<int64_t>(b) * g.a.max_pages;
-    for (int t = k.lo / kTile + kWaves * s0 + wave, s = s0; s < s1 && t < t_end; ++s, t += kWaves) {
-      const int slot = g.tiles_per_page == 1 ? t : static_cast<int>(__umulhi(t, g.page_inv));
-      const int page = __builtin_amdgcn_readfirstlane(table[slot]);
-      if (page < 0 || page >= g.c.n_pages) continue;
-      typename Wave<D, G, NQ>::Raw raw;
-      w.load(g, page, t - slot * g.tiles_per_page, h, raw);
-      if (t * kTile >= w.all_lo && t * kTile + kTile <= w.all_hi)
-        w.template tile<false>(raw, t * kTile, g.scale2);
+    w.scales = &scales[wave];
+    if constexpr (W::kShared) w.shared = space.q;
+    w.begin(g, k, h, wave);
+    if constexpr (W::kShared) __syncthreads();
+    const int t_first = k.lo / kTile + kWaves * s0 + wave;
+    const int t_end = min((k.hi + kTile - 1) / kTile, k.lo / kTile + kWaves * s1);
+    if (t_first < t_end) {
+      if (NQ > 1 && k.rows <= 16)
+        w.template tiles<1>(g, k, h, t_first, t_end);
       else
-        w.template tile<true>(raw, t * kTile, g.scale2);
+        w.template tiles<NQ>(g, k, h, t_first, t_end);
     }
     w.finish();
 
@@ -527,6 +654,7 @@ __global__ __launch_bounds__(kThreads) void kv4_attention_kernel(Args g) {
       }
     }
     if (s0 == 0 && s1 < own) cut = {wg_of(at + own - 1, steps, wgs), h, k.c0, k.row0, k.rows};
+    if constexpr (W::kShared) __syncthreads();
     at += s1 - s0;
     if (s1 == own && h == n_kv - 1) ++item;
   }
@@ -579,15 +707,15 @@ __global__ __launch_bounds__(kThreads) void kv4_join_kernel(Args g) {
 }
 
 // Rows of a row block: 16, 32 or 64, as many as a sequence's new tokens fill.
-Plan plan_of(int64_t T, int64_t B, int n_q, int n_kv, int head_dim, int max_q) {
+Plan plan_of(int64_t T, int64_t B, int n_q, int n_kv, int head_dim, int max_q, int group) {
   const int64_t heads = n_q / n_kv;
   const int64_t most = max_q > 0 ? max_q * heads : (T * heads + B - 1) / B;
   Plan p;
-  p.nq = most <= 16 ? 1 : most <= 32 ? 2 : 4;
+  p.nq = std::min(most <= 16 ? 1 : most <= 32 ? 2 : 4, most_nq(head_dim));
   p.per_sequence = max_q > 0 && max_q * heads <= 16 * p.nq && B <= kListed;
   p.items = static_cast<int>(p.per_sequence ? B : T * heads / (16 * p.nq) + std::min(T, B));
   p.join_rows = static_cast<int>(max_q > 0 ? std::min<int64_t>(most, 16 * p.nq) : 16 * p.nq);
-  p.wgs = p.nq == 4 || head_dim == 256 ? 512 : 1024;
+  p.wgs = 256 * waves_of(head_dim, group, p.nq);
   return p;
 }
 
@@ -616,12 +744,16 @@ struct Space {
 
 template <int D, int G>
 void launch(const Args& g, const Plan& p, hipStream_t stream) {
+  auto run = [&](auto nq) {
+    if constexpr (decltype(nq)::value <= most_nq(D))
+      kv4_attention_kernel<D, G, decltype(nq)::value><<<g.wgs, kThreads, 0, stream>>>(g);
+  };
   if (p.nq == 1)
-    kv4_attention_kernel<D, G, 1><<<g.wgs, kThreads, 0, stream>>>(g);
+    run(std::integral_constant<int, 1>{});
   else if (p.nq == 2)
-    kv4_attention_kernel<D, G, 2><<<g.wgs, kThreads, 0, stream>>>(g);
+    run(std::integral_constant<int, 2>{});
   else
-    kv4_attention_kernel<D, G, 4><<<g.wgs, kThreads, 0, stream>>>(g);
+    run(std::integral_constant<int, 4>{});
   const dim3 grid(static_cast<unsigned>(p.wgs), static_cast<unsigned>(p.join_rows));
   kv4_join_kernel<D><<<grid, kThreads, 0, stream>>>(g);
 }
@@ -639,11 +771,14 @@ void launch_group(const Args& g, const Plan& p, hipStream_t stream) {
 }  // namespace
 
 size_t kv4_attention_bytes(int64_t T, int64_t B, int n_q, int n_kv, int head_dim, int max_q) {
-  return Space(plan_of(T, B, n_q, n_kv, head_dim, max_q), B, head_dim).all;
+  size_t most = 0;
+  for (int group = 32; group <= 128; group *= 2)
+    most = std::max(most, Space(plan_of(T, B, n_q, n_kv, head_dim, max_q, group), B, head_dim).all);
+  return most;
 }
 
 hipError_t launch_kv4_attention(const Kv4Attention& a, const ln_kv4_cache& c, void* workspace, hipStream_t stream) {
-  const Plan p = plan_of(a.T, a.B, a.n_q, c.n_kv, c.head_dim, a.max_q);
+  const Plan p = plan_of(a.T, a.B, a.n_q, c.n_kv, c.head_dim, a.max_q, c.group);
   const Space sp(p, a.B, c.head_dim);
   auto* ws = static_cast<uint8_t*>(workspace);
   Args g;
