@@ -39,9 +39,10 @@ constexpr int kListed = 512;         // sequences whose steps are summed in LDS
 // 16-row tiles of a row block at most, and the waves a SIMD that the registers are cut for
 // (workgroups a CU, then): as many as need no scratch memory.
 constexpr int most_nq(int D) { return D == 64 ? 4 : D == 128 ? 2 : 1; }
-constexpr int waves_of(int D, int G, int NQ) {
-  if (D == 64) return NQ == 1 ? 4 : NQ == 2 && G == 64 ? 3 : 2;
-  return D == 128 && NQ == 1 && G >= 64 ? 3 : 2;
+constexpr int waves_of(int D, int G, int NQ, bool SOLO) {
+  if (D == 64) return NQ == 1 ? 4 : NQ == 2 ? 3 : 2;
+  if (D == 128 && NQ == 1) return G == 128 ? 4 : 3;
+  return 2;
 }
 
 // A value that all lanes share, as one scalar.
@@ -52,7 +53,8 @@ __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirs
 typedef const __attribute__((address_space(4))) int32_t* Const;
 
 struct Plan {
-  int wgs;           // workgroups that share the steps
+  bool solo;         // the workers that share the steps are waves, not workgroups
+  int workers;
   int items;         // row blocks at most
   bool per_sequence; // one row block a sequence: workgroups sum the steps themselves
   int nq;            // 16-row tiles of a row block
@@ -73,7 +75,7 @@ struct Args {
   int tiles_per_page;
   uint32_t page_inv;  // 2^32 / tiles_per_page, rounded up
   float scale2;       // scale log2 e
-  int wgs, items, per_sequence;
+  int workers, items, per_sequence, step;
   // workspace: first[b] = row blocks before sequence b, before[i] = steps before row block i of
   // one key head, before[n] all of them, seq[i] its sequence; the parts; a workgroup's cut
   int *count, *first, *before, *seq;
@@ -85,8 +87,9 @@ struct Args {
 // of them sees.
 struct Block {
   int b, c0, n, len, row0, rows, lo, hi;
-  __device__ __forceinline__ int steps() const {
-    return max(1, ((hi + kTile - 1) / kTile - lo / kTile + kWaves - 1) / kWaves);
+  // in steps of `tiles` key tiles
+  __device__ __forceinline__ int steps(int tiles) const {
+    return max(1, ((hi + kTile - 1) / kTile - lo / kTile + tiles - 1) / tiles);
   }
 };
 
@@ -114,15 +117,18 @@ __device__ __forceinline__ Block make_block(const Args& g, int b, int rb) {
   return k;
 }
 
-// (sums above 2^30 come of a cu_q that does not rise only)
-constexpr int kMostSteps = 1 << 30;
+// (steps are fewer than 2^31 but where cu_q does not rise)
+constexpr int kMostSteps = 0x7FFFFFFF;
+__device__ __forceinline__ int held(int a, int b, int most) {
+  return static_cast<int>(min(static_cast<uint32_t>(a) + static_cast<uint32_t>(b), static_cast<uint32_t>(most)));
+}
 __device__ __forceinline__ int wave_scan(int v, int most) {
   const int lane = threadIdx.x & 63;
   v = min(v, most);
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
     const int o = __shfl_up(v, d);
-    if (lane >= d) v = min(v + o, most);
+    if (lane >= d) v = held(v, o, most);
   }
   return v;
 }
@@ -140,10 +146,10 @@ __device__ __forceinline__ int block_scan(int v, int* part, int& all, int most) 
   all = 0;
 #pragma unroll
   for (int w = 0; w < WAVES; ++w) {
-    before = min(before + (w < wave ? part[w] : 0), most);
-    all = min(all + part[w], most);
+    before = held(before, w < wave ? part[w] : 0, most);
+    all = held(all, part[w], most);
   }
-  return min(v + before, most);
+  return held(v, before, most);
 }
 
 // The number of entries of the rising list at[0 .. n) that are <= x, less one.
@@ -179,7 +185,7 @@ __global__ __launch_bounds__(kPlanThreads) void kv4_plan_kernel(Args g) {
     const int mine = (n * g.heads + g.rows - 1) / g.rows;
     const int upto = block_scan<kPlanThreads / 64>(mine, part, all, g.items);
     if (b < g.a.B) g.first[b] = min(items + max(upto - mine, 0), g.items);
-    items = min(items + all, g.items);  // (more only if cu_q does not rise)
+    items = held(items, all, g.items);  // (more only if cu_q does not rise)
   }
   __threadfence_block();
   __syncthreads();
@@ -189,13 +195,13 @@ __global__ __launch_bounds__(kPlanThreads) void kv4_plan_kernel(Args g) {
     int mine = 0, b = 0;
     if (i < items) {
       b = place_of(g.first, g.a.B, i, 1);
-      mine = make_block(g, b, i - g.first[b]).steps();
+      mine = make_block(g, b, i - g.first[b]).steps(g.step);
     }
-    const int at = steps + block_scan<kPlanThreads / 64>(mine, part, all, kMostSteps) - mine;
-    if (i < items) g.before[i] = at, g.seq[i] = b;
-    steps += all;
+    const int upto = held(steps, block_scan<kPlanThreads / 64>(mine, part, all, kMostSteps), kMostSteps);
+    if (i < items) g.before[i + 1] = upto, g.seq[i] = b;
+    steps = held(steps, all, kMostSteps);
   }
-  if (tid == 0) g.before[items] = steps, *g.count = items;
+  if (tid == 0) g.before[0] = 0, *g.count = items;
 }
 
 // Eight codes as bf16, exactly: a byte c of 0 .. 15 is c 2^-9 in E4M3.
@@ -218,7 +224,7 @@ template <int D, int G, int NQ>
 struct Wave {
   static constexpr int C = D / 32, NG = D / G, CG = G / 32;
   static constexpr int NP = NG < 2 ? 1 : NG / 2;  // words of scales a lane loads
-  static constexpr bool kShared = NQ > 2;         // the queries' operands in LDS, for all waves
+  static constexpr int NZ = (NG + 3) / 4;
 
   struct alignas(D / 8 < 16 ? D / 8 : 16) Words {
     uint32_t w[C];
@@ -230,22 +236,21 @@ struct Wave {
     uint32_t p[NP];
   };
 
-  uint4 q[kShared ? 1 : NQ][C];
-  uint4 (*shared)[C][64];
+  uint4 q[NQ][C];
   Scales<NG>* scales;
   float q_sum[NQ][NG];      // sum of a query's group, in its lanes
   int first[NQ], last[NQ];  // the keys [first, last) that the lane's query sees
   int all_lo, all_hi;       // the keys that every row sees
-  f32x4_t o[NQ][C][2], z[NQ][NG];
+  f32x4_t o[NQ][C][2];
+  f32x4_t z[NQ][NZ];        // sum of the rounded p s, four groups in turn in a result's rows
   float mid[NQ][NG], m[NQ], l[NQ];
   float x[NQ][2][4];        // a tile's scores
 
-  __device__ __forceinline__ void begin(const Args& g, const Block& k, int h, int wave) {
+  __device__ __forceinline__ void begin(const Args& g, const Block& k, int h) {
     const int lane = threadIdx.x & 63, col = lane & 15, seg = lane >> 4;
     // every row sees what the first does, from where the last one's window begins
     all_hi = max(k.len - k.n + k.row0 / g.heads + 1, 0);
     all_lo = g.a.window > 0 ? max(k.len - k.n + (k.row0 + max(k.rows, 1) - 1) / g.heads + 1 - g.a.window, 0) : 0;
-    const uint4 ones = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
 #pragma unroll
     for (int t = 0; t < NQ; ++t) {
       const int row = k.row0 + min(16 * t + col, max(k.rows, 1) - 1);  // rows past the end follow the last
@@ -254,22 +259,22 @@ struct Wave {
       first[t] = g.a.window > 0 ? max(last[t] - g.a.window, 0) : 0;
       const uint16_t* from = g.a.q + (k.c0 + j) * g.a.q_stride + (h * g.heads + row - j * g.heads) * D + 8 * seg;
       const bool ok = 16 * t + col < k.rows;
-      uint4(&mine)[C] = q[kShared ? 0 : t];
 #pragma unroll
-      for (int c = 0; c < C; ++c) mine[c] = ok ? *reinterpret_cast<const uint4*>(from + 32 * c) : uint4{0, 0, 0, 0};
-      if (kShared && t % kWaves == wave) {
+      for (int c = 0; c < C; ++c) q[t][c] = ok ? *reinterpret_cast<const uint4*>(from + 32 * c) : uint4{0, 0, 0, 0};
+    }
+    const uint4 ones = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
 #pragma unroll
-        for (int c = 0; c < C; ++c) shared[t][c][lane] = mine[c];
-      }
+    for (int t = 0; t < NQ; ++t) {
 #pragma unroll
       for (int i = 0; i < NG; ++i) {
         f32x4_t s = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int c = i * CG; c < (i + 1) * CG; ++c) s = mfma16(ones, mine[c], s);
+        for (int c = i * CG; c < (i + 1) * CG; ++c) s = mfma16(ones, q[t][c], s);
         q_sum[t][i] = s[0];
-        z[t][i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
         mid[t][i] = 0.f;
       }
+#pragma unroll
+      for (int i = 0; i < NZ; ++i) z[t][i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int c = 0; c < C; ++c) o[t][c][0] = o[t][c][1] = f32x4_t{0.f, 0.f, 0.f, 0.f};
       m[t] = kLowest;
@@ -333,7 +338,7 @@ struct Wave {
   // The scores of a tile's keys, of NT tiles of queries.
   template <int NT>
   __device__ __forceinline__ void score(const Raw& r) {
-    const int lane = threadIdx.x & 63, seg = lane >> 4;
+    const int seg = (threadIdx.x & 63) >> 4;
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
 #pragma unroll
@@ -346,7 +351,7 @@ struct Wave {
           const uint32_t w = r.w[s].w[c];
           const uint4 wide = wide_codes(w & 0x0F0F0F0Fu, (w >> 4) & 0x0F0F0F0Fu);
 #pragma unroll
-          for (int t = 0; t < NT; ++t) acc[t] = mfma16(wide, kShared ? shared[t][c][lane] : q[kShared ? 0 : t][c], acc[t]);
+          for (int t = 0; t < NT; ++t) acc[t] = mfma16(wide, q[t][c], acc[t]);
         }
         float step[4], least[4];
         split(&scales->k[i][16 * s + 4 * seg], step, least);
@@ -398,11 +403,11 @@ struct Wave {
         m[t] = now;
         l[t] *= f;
 #pragma unroll
-        for (int i = 0; i < NG; ++i) {
-          mid[t][i] *= f;
+        for (int i = 0; i < NG; ++i) mid[t][i] *= f;
+#pragma unroll
+        for (int i = 0; i < NZ; ++i)
 #pragma unroll
           for (int e = 0; e < 4; ++e) z[t][i][e] *= f;
-        }
 #pragma unroll
         for (int c = 0; c < C; ++c)
 #pragma unroll
@@ -415,9 +420,11 @@ struct Wave {
         l[t] += v;
       }
     }
-    const uint4 ones = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
 #pragma unroll
     for (int i = 0; i < NG; ++i) {
+      // group i's sum goes to the rows that are i modulo four
+      const uint32_t one = NG == 1 || (threadIdx.x & 3) == i % 4 ? 0x3F803F80u : 0u;
+      const uint4 ones = {one, one, one, one};
       float step[2][4], centre[2][4];
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
@@ -436,7 +443,7 @@ struct Wave {
           mid[t][i] = __builtin_fmaf(v, centre[e >> 2][e & 3], mid[t][i]);
         }
         p[t] = uint4{pack_bf16x2(w[0], w[1]), pack_bf16x2(w[2], w[3]), pack_bf16x2(w[4], w[5]), pack_bf16x2(w[6], w[7])};
-        z[t][i] = mfma16(ones, p[t], z[t][i]);
+        z[t][i / 4] = mfma16(ones, p[t], z[t][i / 4]);
       }
 #pragma unroll
       for (int c = i * CG; c < (i + 1) * CG; ++c) {
@@ -461,10 +468,10 @@ struct Wave {
     }
   }
 
-  // The wave's tiles t, t + 4, .. below t_end of a key head. A tile's keys are loaded while the
+  // The wave's tiles t, t + STEP, .. below t_end of a key head. A tile's keys are loaded while the
   // values of the one before are multiplied, its values while its keys are, each into the registers
   // that were just read.
-  template <int NT>
+  template <int NT, int STEP>
   __device__ __forceinline__ void tiles(const Args& g, const Block& k, int h, int t, int t_end) {
     const Const table = (Const)(g.a.block_table + static_cast<int64_t>(k.b) * g.a.max_pages);
     auto slot_of = [&](int t) { return g.tiles_per_page == 1 ? t : static_cast<int>(__umulhi(t, g.page_inv)); };
@@ -483,18 +490,18 @@ struct Wave {
     place(t, slot, table[slot]);
     load_keys(g, row, par, keys);
     load_values(g, row, par, values);
-    int next_slot = slot_of(min(t + kWaves, t_end - 1)), page = table[next_slot];
+    int next_slot = slot_of(min(t + STEP, t_end - 1)), page = table[next_slot];
     bool more;
     do {
       const int key0 = t * kTile, lo = gone ? key0 + kTile : k.lo;
       const bool border = gone || key0 < all_lo || key0 + kTile > all_hi;
-      t += kWaves;
+      t += STEP;
       more = t < t_end;
       put_key_scales(keys, key0, lo, k.hi);
       score<NT>(keys);
       if (more) place(t, next_slot, page);  // (the last tile is loaded again: counted waits need no two ways)
       load_keys(g, row, par, keys);
-      next_slot = slot_of(min(t + kWaves, t_end - 1));
+      next_slot = slot_of(min(t + STEP, t_end - 1));
       page = table[next_slot];
       if (border) hide<NT>(key0, lo);
       put_value_scales(values, key0, lo, k.hi);
@@ -514,7 +521,7 @@ struct Wave {
         float c = mid[t][i];
         c += __shfl_xor(c, 16);
         c += __shfl_xor(c, 32);
-        c = __builtin_fmaf(-8.f, z[t][i][0], c);
+        c = __builtin_fmaf(-8.f, z[t][i / 4][i % 4], c);
 #pragma unroll
         for (int k = i * CG; k < (i + 1) * CG; ++k)
 #pragma unroll
@@ -531,24 +538,47 @@ struct Joined {
   float m[kWaves][16], l[kWaves][16];
 };
 
-__device__ __forceinline__ void store4(uint16_t* p, float a, float b, float c, float d) {
-  *reinterpret_cast<uint2*>(p) = uint2{pack_bf16x2(a, b), pack_bf16x2(c, d)};
-}
+template <>
+struct Joined<0> {};
 
-template <int D, int G, int NQ>
-__global__ __launch_bounds__(kThreads, waves_of(D, G, NQ)) void kv4_attention_kernel(Args g) {
+// Where a row of a row block and head goes: y and lse, or a part.
+struct Out {
+  const Args& g;
+  const Block& k;
+  int h;
+  bool whole;
+  int64_t slot;
+
+  // Four sums from element d on, of weights 2^(score - m) that add up to l.
+  template <int D>
+  __device__ __forceinline__ void put(int row, int d, float m, float l, const float4& o) const {
+    if (whole) {
+      const int j = (k.row0 + row) / g.heads;
+      const int64_t out = static_cast<int64_t>(k.c0 + j) * g.a.n_q + h * g.heads + k.row0 + row - j * g.heads;
+      const float inv = l > 0.f ? 1.f / l : 0.f;
+      *reinterpret_cast<uint2*>(g.a.y + out * D + d) =
+          uint2{pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv)};
+      if (g.a.lse != nullptr && d == 0)
+        g.a.lse[out] = l > 0.f ? (m + __builtin_log2f(l)) * 0.69314718055994531f : -__builtin_inff();
+    } else {
+      *reinterpret_cast<float4*>(g.part_o + (slot * g.rows + row) * D + d) = o;
+      if (d == 0) *reinterpret_cast<float2*>(g.part_ml + (slot * g.rows + row) * 2) = float2{m, l};
+    }
+  }
+};
+
+// SOLO: the waves are workers on their own, each with its share of tiles, and join nothing.
+// Otherwise a workgroup is one, and its waves take every fourth tile of its share.
+template <int D, int G, int NQ, bool SOLO>
+__global__ __launch_bounds__(kThreads, waves_of(D, G, NQ, SOLO)) void kv4_attention_kernel(Args g) {
   typedef Wave<D, G, NQ> W;
-  constexpr int C = D / 32;
-  __shared__ union {
-    Joined<D> joined;
-    uint4 q[W::kShared ? NQ : 1][C][64];
-  } space;
-  Joined<D>& joined = space.joined;
+  constexpr int C = D / 32, kStep = SOLO ? 1 : kWaves;
+  __shared__ Joined<SOLO ? 0 : D> joined;
   __shared__ Scales<W::NG> scales[kWaves];
   __shared__ int listed[kListed + 1];
   __shared__ int part[kWaves];
   const int tid = threadIdx.x, wave = uniform(tid >> 6), lane = tid & 63;
-  const int n_kv = g.c.n_kv;
+  const int col = lane & 15, seg = lane >> 4, n_kv = g.c.n_kv;
 
   // the steps before every row block
   int items;
@@ -558,25 +588,26 @@ __global__ __launch_bounds__(kThreads, waves_of(D, G, NQ)) void kv4_attention_ke
     int steps = 0, all;
     for (int b0 = 0; b0 < items; b0 += kThreads) {
       const int b = b0 + tid;
-      const int mine = b < items ? make_block(g, b, 0).steps() : 0;
-      const int at = steps + block_scan<kWaves>(mine, part, all, kMostSteps);
-      if (b < items) listed[b + 1] = at;
-      steps += all;
+      const int mine = b < items ? make_block(g, b, 0).steps(g.step) : 0;
+      const int upto = held(steps, block_scan<kWaves>(mine, part, all, kMostSteps), kMostSteps);
+      if (b < items) listed[b + 1] = upto;
+      steps = held(steps, all, kMostSteps);
     }
     if (tid == 0) listed[0] = 0;
     __syncthreads();
     before = listed;
   } else {
-    items = *g.count;
+    items = *(Const)g.count;
     before = g.before;
   }
-  const int64_t steps = static_cast<int64_t>(before[items]) * n_kv;
-  const int wgs = sharing(steps, g.wgs), wg = blockIdx.x;
-  if (wg >= wgs) {
-    if (tid == 0) g.cut[wg].last = 0;
+  const int64_t steps = static_cast<int64_t>(uniform(before[items])) * n_kv;
+  const int workers = sharing(steps, g.workers), me = SOLO ? kWaves * blockIdx.x + wave : blockIdx.x;
+  const bool writer = SOLO ? lane == 0 : tid == 0;
+  if (me >= workers) {
+    if (writer) g.cut[me].last = 0;
     return;
   }
-  const int64_t end = step_of(wg + 1, steps, wgs), begin = step_of(wg, steps, wgs);
+  const int64_t end = step_of(me + 1, steps, workers), begin = step_of(me, steps, workers);
 
   Cut cut = {0, 0, 0, 0, 0};
   int64_t at = begin;
@@ -585,126 +616,140 @@ __global__ __launch_bounds__(kThreads, waves_of(D, G, NQ)) void kv4_attention_ke
     const int base = uniform(before[item]);
     const int own = uniform(before[item + 1]) - base;  // steps of the row block
     const int64_t in = at - static_cast<int64_t>(base) * n_kv;
-    const int h = uniform(static_cast<int>(in / own));
+    const int h = uniform(in >> 32 ? static_cast<int>(in / own)
+                                   : static_cast<int>(static_cast<uint32_t>(in) / static_cast<uint32_t>(own)));
     const int s0 = uniform(static_cast<int>(in - static_cast<int64_t>(h) * own));
     const int s1 = uniform(static_cast<int>(min(static_cast<int64_t>(own), s0 + end - at)));
-    const int b = g.per_sequence ? item : uniform(g.seq[item]);
-    Block k = make_block(g, b, g.per_sequence ? 0 : item - uniform(g.first[b]));
+    const int b = g.per_sequence ? item : ((Const)g.seq)[item];
+    Block k = make_block(g, b, g.per_sequence ? 0 : item - ((Const)g.first)[b]);
     k.c0 = uniform(k.c0), k.n = uniform(k.n), k.len = uniform(k.len), k.row0 = uniform(k.row0);
     k.rows = uniform(k.rows), k.lo = uniform(k.lo), k.hi = uniform(k.hi);
 
-    Wave<D, G, NQ> w;
+    W w;
     w.scales = &scales[wave];
-    if constexpr (W::kShared) w.shared = space.q;
-    w.begin(g, k, h, wave);
-    if constexpr (W::kShared) __syncthreads();
-    const int t_first = k.lo / kTile + kWaves * s0 + wave;
-    const int t_end = min((k.hi + kTile - 1) / kTile, k.lo / kTile + kWaves * s1);
+    w.begin(g, k, h);
+    const int t_first = k.lo / kTile + kStep * s0 + (SOLO ? 0 : wave);
+    const int t_end = min((k.hi + kTile - 1) / kTile, k.lo / kTile + kStep * s1);
     if (t_first < t_end) {
       if (NQ > 1 && k.rows <= 16)
-        w.template tiles<1>(g, k, h, t_first, t_end);
+        w.template tiles<1, kStep>(g, k, h, t_first, t_end);
       else
-        w.template tiles<NQ>(g, k, h, t_first, t_end);
+        w.template tiles<NQ, kStep>(g, k, h, t_first, t_end);
     }
     w.finish();
 
-    // The waves' sums, 16 rows at a time. Whole: y. A part: slot 1 of the workgroup where the
-    // row block begins in its share, 0 where it began before.
+    // Whole: y. A part: slot 1 of the worker where the row block begins in its share, 0 where
+    // it began before.
     const bool whole = s0 == 0 && s1 == own;
-    const int64_t slot = 2 * static_cast<int64_t>(wg) + (s0 == 0 ? 1 : 0);
+    const int64_t slot = 2 * static_cast<int64_t>(me) + (s0 == 0 ? 1 : 0);
+    const Out to = {g, k, h, whole, slot};
 #pragma unroll
     for (int t = 0; t < NQ; ++t) {
       if (16 * t >= k.rows) break;
-      __syncthreads();
-      const int col = lane & 15, seg = lane >> 4;
+      if constexpr (SOLO) {
+        const int row = 16 * t + col;
+        if (row < k.rows) {
 #pragma unroll
-      for (int c = 0; c < C; ++c)
+          for (int c = 0; c < C; ++c)
 #pragma unroll
-        for (int e = 0; e < 4; e += 2)
-          *reinterpret_cast<float4*>(&joined.o[wave][col][32 * c + 8 * seg + 2 * e]) =
-              float4{w.o[t][c][0][e], w.o[t][c][1][e], w.o[t][c][0][e + 1], w.o[t][c][1][e + 1]};
-      if (seg == 0) joined.m[wave][col] = w.m[t], joined.l[wave][col] = w.l[t];
-      __syncthreads();
-      for (int u = tid; u < 16 * (D / 4); u += kThreads) {
-        const int r = u / (D / 4), d = u % (D / 4) * 4, row = 16 * t + r;
-        if (row >= k.rows) break;
-        float m = joined.m[0][r];
-#pragma unroll
-        for (int v = 1; v < kWaves; ++v) m = fmaxf(m, joined.m[v][r]);
-        float l = 0.f;
-        float4 o = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int v = 0; v < kWaves; ++v) {
-          const float f = __builtin_amdgcn_exp2f(joined.m[v][r] - m);
-          const float4 p = *reinterpret_cast<const float4*>(&joined.o[v][r][d]);
-          l += f * joined.l[v][r];
-          o.x += f * p.x, o.y += f * p.y, o.z += f * p.z, o.w += f * p.w;
+            for (int e = 0; e < 4; e += 2)
+              to.template put<D>(row, 32 * c + 8 * seg + 2 * e, w.m[t], w.l[t],
+                                 float4{w.o[t][c][0][e], w.o[t][c][1][e], w.o[t][c][0][e + 1], w.o[t][c][1][e + 1]});
         }
-        if (whole) {
-          const int j = (k.row0 + row) / g.heads;
-          const int64_t out = static_cast<int64_t>(k.c0 + j) * g.a.n_q + h * g.heads + k.row0 + row - j * g.heads;
-          const float inv = l > 0.f ? 1.f / l : 0.f;
-          store4(g.a.y + out * D + d, o.x * inv, o.y * inv, o.z * inv, o.w * inv);
-          if (g.a.lse != nullptr && d == 0)
-            g.a.lse[out] = l > 0.f ? (m + __builtin_log2f(l)) * 0.69314718055994531f : -__builtin_inff();
-        } else {
-          *reinterpret_cast<float4*>(g.part_o + (slot * g.rows + row) * D + d) = o;
-          if (d == 0) *reinterpret_cast<float2*>(g.part_ml + (slot * g.rows + row) * 2) = float2{m, l};
+      } else {
+        __syncthreads();
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+          for (int e = 0; e < 4; e += 2)
+            *reinterpret_cast<float4*>(&joined.o[wave][col][32 * c + 8 * seg + 2 * e]) =
+                float4{w.o[t][c][0][e], w.o[t][c][1][e], w.o[t][c][0][e + 1], w.o[t][c][1][e + 1]};
+        if (seg == 0) joined.m[wave][col] = w.m[t], joined.l[wave][col] = w.l[t];
+        __syncthreads();
+        for (int u = tid; u < 16 * (D / 4); u += kThreads) {
+          const int r = u / (D / 4), d = u % (D / 4) * 4, row = 16 * t + r;
+          if (row >= k.rows) break;
+          float m = joined.m[0][r];
+#pragma unroll
+          for (int v = 1; v < kWaves; ++v) m = fmaxf(m, joined.m[v][r]);
+          float l = 0.f;
+          float4 o = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int v = 0; v < kWaves; ++v) {
+            const float f = __builtin_amdgcn_exp2f(joined.m[v][r] - m);
+            const float4 p = *reinterpret_cast<const float4*>(&joined.o[v][r][d]);
+            l += f * joined.l[v][r];
+            o.x += f * p.x, o.y += f * p.y, o.z += f * p.z, o.w += f * p.w;
+          }
+          to.template put<D>(row, d, m, l, o);
         }
       }
     }
-    if (s0 == 0 && s1 < own) cut = {wg_of(at + own - 1, steps, wgs), h, k.c0, k.row0, k.rows};
-    if constexpr (W::kShared) __syncthreads();
+    if (s0 == 0 && s1 < own) cut = {wg_of(at + own - 1, steps, workers), h, k.c0, k.row0, k.rows};
     at += s1 - s0;
     if (s1 == own && h == n_kv - 1) ++item;
   }
-  if (tid == 0) g.cut[wg] = cut;
+  if (writer) g.cut[me] = cut;
 }
 
-// Joins the parts of the row blocks that were cut: one workgroup to a row of one, its threads
-// in groups of D / 4 to every n-th part.
+// Joins the parts of the row blocks that were cut, a workgroup to a worker's cut (and every n-th
+// of its rows). Its threads in groups of D / 4: kGroups / rows_at of them to every n-th part of
+// one row, rows_at rows at a time.
 template <int D>
-__global__ __launch_bounds__(kThreads) void kv4_join_kernel(Args g) {
+__global__ __launch_bounds__(kThreads) void kv4_join_kernel(Args g, int rows_at) {
   constexpr int kLanes = D / 4, kGroups = kThreads / kLanes;
   __shared__ float4 sum[kGroups][kLanes];
   __shared__ float top[kGroups], all[kGroups];
-  const int w0 = blockIdx.x, row = blockIdx.y;
+  const int w0 = blockIdx.x;
   const Cut k = g.cut[w0];
   const int w1 = k.last, h = k.head;
-  if (w1 == 0 || row >= k.rows) return;
+  if (w1 == 0) return;
 
   const int grp = threadIdx.x / kLanes, d = threadIdx.x % kLanes * 4;
-  float m = kLowest, l = 0.f;
-  float4 o = {0.f, 0.f, 0.f, 0.f};
-  for (int w = w0 + grp; w <= w1; w += kGroups) {
-    const int64_t at = (2 * static_cast<int64_t>(w) + (w == w0 ? 1 : 0)) * g.rows + row;
-    const float2 ml = *reinterpret_cast<const float2*>(g.part_ml + at * 2);
-    const float4 p = *reinterpret_cast<const float4*>(g.part_o + at * D + d);
-    const float now = fmaxf(m, ml.x), f = __builtin_amdgcn_exp2f(m - now), e = __builtin_amdgcn_exp2f(ml.x - now);
-    m = now;
-    l = l * f + ml.y * e;
-    o.x = o.x * f + p.x * e, o.y = o.y * f + p.y * e, o.z = o.z * f + p.z * e, o.w = o.w * f + p.w * e;
+  const int own = grp % rows_at, turn = grp / rows_at, turns = kGroups / rows_at;
+  for (int row0 = blockIdx.y * rows_at; row0 < k.rows; row0 += gridDim.y * rows_at) {
+    const int row = row0 + own;
+    float m = kLowest, l = 0.f;
+    float4 o = {0.f, 0.f, 0.f, 0.f};
+    if (row < k.rows) {
+      for (int w = w0 + turn; w <= w1; w += turns) {
+        const int64_t at = (2 * static_cast<int64_t>(w) + (w == w0 ? 1 : 0)) * g.rows + row;
+        const float2 ml = *reinterpret_cast<const float2*>(g.part_ml + at * 2);
+        const float4 p = *reinterpret_cast<const float4*>(g.part_o + at * D + d);
+        const float now = fmaxf(m, ml.x), f = __builtin_amdgcn_exp2f(m - now), e = __builtin_amdgcn_exp2f(ml.x - now);
+        m = now;
+        l = l * f + ml.y * e;
+        o.x = o.x * f + p.x * e, o.y = o.y * f + p.y * e, o.z = o.z * f + p.z * e, o.w = o.w * f + p.w * e;
+      }
+    }
+    if (turns > 1) {
+      sum[grp][d / 4] = o;
+      if (d == 0) top[grp] = m, all[grp] = l;
+      __syncthreads();
+      for (int v = own; v < kGroups; v += rows_at) m = fmaxf(m, top[v]);
+      l = 0.f;
+      o = float4{0.f, 0.f, 0.f, 0.f};
+      if (turn == 0) {
+        for (int v = own; v < kGroups; v += rows_at) {
+          const float e = __builtin_amdgcn_exp2f(top[v] - m);
+          const float4 p = sum[v][d / 4];
+          l += all[v] * e;
+          o.x += p.x * e, o.y += p.y * e, o.z += p.z * e, o.w += p.w * e;
+        }
+      }
+      __syncthreads();
+    }
+    if (turn == 0 && row < k.rows) {
+      Block b;
+      b.c0 = k.c0, b.row0 = k.row0;
+      const Out to = {g, b, h, true, 0};
+      to.template put<D>(row, d, m, l, o);
+    }
   }
-  sum[grp][d / 4] = o;
-  if (d == 0) top[grp] = m, all[grp] = l;
-  __syncthreads();
-  if (grp != 0) return;
-  for (int v = 0; v < kGroups; ++v) m = fmaxf(m, top[v]);
-  l = 0.f;
-  o = float4{0.f, 0.f, 0.f, 0.f};
-  for (int v = 0; v < kGroups; ++v) {
-    const float e = __builtin_amdgcn_exp2f(top[v] - m);
-    const float4 p = sum[v][d / 4];
-    l += all[v] * e;
-    o.x += p.x * e, o.y += p.y * e, o.z += p.z * e, o.w += p.w * e;
-  }
-  const int j = (k.row0 + row) / g.heads;
-  const int64_t out = static_cast<int64_t>(k.c0 + j) * g.a.n_q + h * g.heads + k.row0 + row - j * g.heads;
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-  store4(g.a.y + out * D + d, o.x * inv, o.y * inv, o.z * inv, o.w * inv);
-  if (g.a.lse != nullptr && d == 0)
-    g.a.lse[out] = l > 0.f ? (m + __builtin_log2f(l)) * 0.69314718055994531f : -__builtin_inff();
 }
+
+// Workers of their own are waves where there are row blocks enough that each has few parts.
+bool solo_of(int64_t items, int n_kv) { return items * n_kv >= 1024; }
 
 // Rows of a row block: 16, 32 or 64, as many as a sequence's new tokens fill.
 Plan plan_of(int64_t T, int64_t B, int n_q, int n_kv, int head_dim, int max_q, int group) {
@@ -715,7 +760,8 @@ Plan plan_of(int64_t T, int64_t B, int n_q, int n_kv, int head_dim, int max_q, i
   p.per_sequence = max_q > 0 && max_q * heads <= 16 * p.nq && B <= kListed;
   p.items = static_cast<int>(p.per_sequence ? B : T * heads / (16 * p.nq) + std::min(T, B));
   p.join_rows = static_cast<int>(max_q > 0 ? std::min<int64_t>(most, 16 * p.nq) : 16 * p.nq);
-  p.wgs = 256 * waves_of(head_dim, group, p.nq);
+  p.solo = solo_of(p.items, n_kv);
+  p.workers = 256 * waves_of(head_dim, group, p.nq, p.solo) * (p.solo ? kWaves : 1);
   return p;
 }
 
@@ -724,7 +770,7 @@ size_t up256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
 struct Space {
   size_t count, first, before, seq, part_o, part_ml, cut, all;
   Space(const Plan& p, int64_t B, int head_dim) {
-    const size_t rows = static_cast<size_t>(p.wgs) * 2 * 16 * p.nq;
+    const size_t rows = static_cast<size_t>(p.workers) * 2 * 16 * p.nq;
     size_t at = 0;
     auto take = [&](size_t bytes) {
       const size_t here = at;
@@ -737,7 +783,7 @@ struct Space {
     seq = take(static_cast<size_t>(p.items) * 4);
     part_o = take(rows * head_dim * 4);
     part_ml = take(rows * 8);
-    cut = take(static_cast<size_t>(p.wgs) * sizeof(Cut));
+    cut = take(static_cast<size_t>(p.workers) * sizeof(Cut));
     all = at;
   }
 };
@@ -745,8 +791,13 @@ struct Space {
 template <int D, int G>
 void launch(const Args& g, const Plan& p, hipStream_t stream) {
   auto run = [&](auto nq) {
-    if constexpr (decltype(nq)::value <= most_nq(D))
-      kv4_attention_kernel<D, G, decltype(nq)::value><<<g.wgs, kThreads, 0, stream>>>(g);
+    constexpr int NQ = decltype(nq)::value;
+    if constexpr (NQ <= most_nq(D)) {
+      if (p.solo)
+        kv4_attention_kernel<D, G, NQ, true><<<p.workers / kWaves, kThreads, 0, stream>>>(g);
+      else
+        kv4_attention_kernel<D, G, NQ, false><<<p.workers, kThreads, 0, stream>>>(g);
+    }
   };
   if (p.nq == 1)
     run(std::integral_constant<int, 1>{});
@@ -754,8 +805,10 @@ void launch(const Args& g, const Plan& p, hipStream_t stream) {
     run(std::integral_constant<int, 2>{});
   else
     run(std::integral_constant<int, 4>{});
-  const dim3 grid(static_cast<unsigned>(p.wgs), static_cast<unsigned>(p.join_rows));
-  kv4_join_kernel<D><<<grid, kThreads, 0, stream>>>(g);
+  // Few parts of each row block: a group of threads a row. Many: all of them to one row.
+  const int rows_at = p.solo ? kThreads / (D / 4) : 1;
+  const dim3 grid(static_cast<unsigned>(p.workers), static_cast<unsigned>(p.solo ? 1 : p.join_rows));
+  kv4_join_kernel<D><<<grid, kThreads, 0, stream>>>(g, rows_at);
 }
 
 template <int D>
@@ -789,9 +842,10 @@ hipError_t launch_kv4_attention(const Kv4Attention& a, const ln_kv4_cache& c, vo
   g.tiles_per_page = c.page_size / kTile;
   g.page_inv = static_cast<uint32_t>(((uint64_t(1) << 32) + g.tiles_per_page - 1) / g.tiles_per_page);
   g.scale2 = a.scale * 1.4426950408889634f;
-  g.wgs = p.wgs;
+  g.workers = p.workers;
   g.items = p.items;
   g.per_sequence = p.per_sequence;
+  g.step = p.solo ? 1 : kWaves;
   g.count = reinterpret_cast<int*>(ws + sp.count);
   g.first = reinterpret_cast<int*>(ws + sp.first);
   g.before = reinterpret_cast<int*>(ws + sp.before);
