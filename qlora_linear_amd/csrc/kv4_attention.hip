@@ -41,7 +41,7 @@ constexpr int kListed = 512;         // sequences whose steps are summed in LDS
 constexpr int most_nq(int D) { return D == 64 ? 4 : D == 128 ? 2 : 1; }
 constexpr int waves_of(int D, int G, int NQ, bool SOLO) {
   if (D == 64) return NQ == 1 ? 4 : NQ == 2 ? 3 : 2;
-  if (D == 128 && NQ == 1) return G == 128 ? 4 : 3;
+  if (D == 128 && NQ == 1) return 3;
   return 2;
 }
 
@@ -87,9 +87,11 @@ struct Args {
 // of them sees.
 struct Block {
   int b, c0, n, len, row0, rows, lo, hi;
-  // in steps of `tiles` key tiles
+  // In steps of `tiles` key tiles, one more for what a row block costs besides (its queries, its
+  // place, its output: 2 to 3 us, a step's time. Without it the workers with the shortest sequences
+  // ended last: 96 x 40 heads XX -> YY us).
   __device__ __forceinline__ int steps(int tiles) const {
-    return max(1, ((hi + kTile - 1) / kTile - lo / kTile + tiles - 1) / tiles);
+    return 1 + ((hi + kTile - 1) / kTile - lo / kTile + tiles - 1) / tiles;
   }
 };
 
@@ -213,11 +215,12 @@ __device__ __forceinline__ uint4 wide_codes(uint32_t lo, uint32_t hi) {
                two(hi, std::true_type{})};
 }
 
-// The steps and least values of a wave's tile, in LDS: they come as one word a lane and are read
-// as four keys', so that registers hold them only while they are used.
+// The steps of a wave's tile, and its least values or (of values) those of code 8, in LDS: they
+// come as one word a lane, widen there once, and are read as four keys' at a time, so that
+// registers hold them only while they are used. Keys' are in units of 2^x's argument.
 template <int NG>
 struct Scales {
-  uint32_t k[NG][kTile], v[NG][kTile];
+  float step[2][NG][kTile], base[2][NG][kTile];  // [keys, values]
 };
 
 template <int D, int G, int NQ>
@@ -309,30 +312,33 @@ struct Wave {
     }
   }
   // Scales of values that no row sees may be no numbers: keys outside [lo, hi) get zeros.
-  __device__ __forceinline__ void put_key_scales(const Raw& r, int key0, int lo, int hi) {
-    const int lane = threadIdx.x & 63;
+  __device__ __forceinline__ void put_key_scales(const Raw& r, int key0, int lo, int hi, float scale2) {
     if constexpr (NG == 1) {
-      const int key = key0 + lane % kTile;
-      (&scales->k[0][0])[lane] = lane >= kTile && (key < lo || key >= hi) ? 0u : r.p[0];
+      const int lane = threadIdx.x & 63, key = key0 + lane % kTile;
+      const bool value = lane >= kTile;
+      put(lane, value && (key < lo || key >= hi) ? 0u : r.p[0], value ? 1.f : scale2, value ? 8.f : 0.f);
     } else {
 #pragma unroll
-      for (int i = 0; i < NP; ++i) (&scales->k[0][0])[64 * i + lane] = r.p[i];
+      for (int i = 0; i < NP; ++i) put(64 * i + (threadIdx.x & 63), r.p[i], scale2, 0.f);
     }
   }
   __device__ __forceinline__ void put_value_scales(const Raw& r, int key0, int lo, int hi) {
     if constexpr (NG > 1) {
       const int lane = threadIdx.x & 63, key = key0 + lane % kTile;
 #pragma unroll
-      for (int i = 0; i < NP; ++i) (&scales->v[0][0])[64 * i + lane] = key < lo || key >= hi ? 0u : r.p[i];
+      for (int i = 0; i < NP; ++i) put(NG * kTile + 64 * i + lane, key < lo || key >= hi ? 0u : r.p[i], 1.f, 8.f);
     }
   }
+  __device__ __forceinline__ void put(int at, uint32_t word, float times, float code) {
+    const float step = __uint_as_float(word << 16), least = __uint_as_float(word & 0xFFFF0000u);
+    (&scales->step[0][0][0])[at] = step * times;
+    (&scales->base[0][0][0])[at] = __builtin_fmaf(code, step, least) * times;
+  }
 
-  // Steps and least values of four keys.
-  static __device__ __forceinline__ void split(const uint32_t* from, float (&s)[4], float (&least)[4]) {
-    const uint4 p = *reinterpret_cast<const uint4*>(from);
-    const uint32_t w[4] = {p.x, p.y, p.z, p.w};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) s[e] = __uint_as_float(w[e] << 16), least[e] = __uint_as_float(w[e] & 0xFFFF0000u);
+  // Four keys' floats.
+  static __device__ __forceinline__ void four(const float* from, float (&v)[4]) {
+    const float4 p = *reinterpret_cast<const float4*>(from);
+    v[0] = p.x, v[1] = p.y, v[2] = p.z, v[3] = p.w;
   }
 
   // The scores of a tile's keys, of NT tiles of queries.
@@ -354,7 +360,8 @@ struct Wave {
           for (int t = 0; t < NT; ++t) acc[t] = mfma16(wide, q[t][c], acc[t]);
         }
         float step[4], least[4];
-        split(&scales->k[i][16 * s + 4 * seg], step, least);
+        four(&scales->step[0][i][16 * s + 4 * seg], step);
+        four(&scales->base[0][i][16 * s + 4 * seg], least);
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -388,14 +395,13 @@ struct Wave {
 
   // The tile's part of the sums.
   template <int NT>
-  __device__ __forceinline__ void sum(const Raw& r, float scale2) {
+  __device__ __forceinline__ void sum(const Raw& r) {
     const int seg = (threadIdx.x & 63) >> 4;
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       float top = x[t][0][0];
 #pragma unroll
       for (int e = 1; e < 8; ++e) top = fmaxf(top, x[t][e >> 2][e & 3]);
-      top *= scale2;
       if (__any(top > m[t] + 8.f)) {
         top = fmaxf(top, __shfl_xor(top, 16));
         top = fmaxf(top, __shfl_xor(top, 32));
@@ -416,7 +422,7 @@ struct Wave {
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         float& v = x[t][e >> 2][e & 3];
-        v = __builtin_amdgcn_exp2f(__builtin_fmaf(v, scale2, -m[t]));
+        v = __builtin_amdgcn_exp2f(v - m[t]);
         l[t] += v;
       }
     }
@@ -428,9 +434,8 @@ struct Wave {
       float step[2][4], centre[2][4];
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
-        split(&scales->v[i][16 * s + 4 * seg], step[s], centre[s]);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) centre[s][e] = __builtin_fmaf(8.f, step[s][e], centre[s][e]);
+        four(&scales->step[1][i][16 * s + 4 * seg], step[s]);
+        four(&scales->base[1][i][16 * s + 4 * seg], centre[s]);
       }
       uint4 p[NT];
 #pragma unroll
@@ -497,7 +502,7 @@ struct Wave {
       const bool border = gone || key0 < all_lo || key0 + kTile > all_hi;
       t += STEP;
       more = t < t_end;
-      put_key_scales(keys, key0, lo, k.hi);
+      put_key_scales(keys, key0, lo, k.hi, g.scale2);
       score<NT>(keys);
       if (more) place(t, next_slot, page);  // (the last tile is loaded again: counted waits need no two ways)
       load_keys(g, row, par, keys);
@@ -505,7 +510,7 @@ struct Wave {
       page = table[next_slot];
       if (border) hide<NT>(key0, lo);
       put_value_scales(values, key0, lo, k.hi);
-      sum<NT>(values, g.scale2);
+      sum<NT>(values);
       load_values(g, row, par, values);
     } while (more);
   }
@@ -628,8 +633,8 @@ __global__ __launch_bounds__(kThreads, waves_of(D, G, NQ, SOLO)) void kv4_attent
     W w;
     w.scales = &scales[wave];
     w.begin(g, k, h);
-    const int t_first = k.lo / kTile + kStep * s0 + (SOLO ? 0 : wave);
-    const int t_end = min((k.hi + kTile - 1) / kTile, k.lo / kTile + kStep * s1);
+    const int t_first = k.lo / kTile + kStep * max(s0 - 1, 0) + (SOLO ? 0 : wave);  // (step 0 has no keys)
+    const int t_end = min((k.hi + kTile - 1) / kTile, k.lo / kTile + kStep * (s1 - 1));
     if (t_first < t_end) {
       if (NQ > 1 && k.rows <= 16)
         w.template tiles<1, kStep>(g, k, h, t_first, t_end);
