@@ -129,7 +129,7 @@ int kv4_read(int64_t T, const int64_t* slots, const ln_kv4_cache* cache, int out
  *               one each
  * n_q a multiple of n_kv, up to LN_KV4_MAX_HEADS. 0 <= T < 2^24, T n_q < 2^31, 1 <= B < 2^20,
  * max_pages >= 1, max_pages page_size <= 2^30, and row blocks of 16 times tiles of 32 keys,
- * (T n_q / n_kv / 16 + B) (max_pages page_size / 32 + 2), fewer than 2^31.
+ * (T n_q / n_kv / 16 + B) (max_pages page_size / 32 + 2), fewer than 2^36.
  */
 int kv4_attention(int64_t T, int64_t B, int32_t n_q, const uint16_t* q, int64_t q_stride, const int32_t* cu_q,
                   int32_t max_q, const int32_t* lens, const int32_t* block_table, int64_t max_pages, int32_t window,

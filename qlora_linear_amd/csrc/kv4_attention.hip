@@ -34,6 +34,7 @@ constexpr int kThreads = 256;
 constexpr int kWaves = 4;
 constexpr int kTile = 32;             // keys of a wave's tile
 constexpr float kLowest = -3.0e38f;   // the maximum of no keys
+constexpr float kBar = 8.f;           // p stays below 2^8
 constexpr int kListed = 512;         // sequences whose steps are summed in LDS
 
 // 16-row tiles of a row block at most, and the waves a SIMD that the registers are cut for
@@ -47,6 +48,10 @@ constexpr int waves_of(int D, int G, int NQ, bool SOLO) {
 
 // A value that all lanes share, as one scalar.
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ int64_t uniform(int64_t v) {
+  const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<int>(v));
+  return (static_cast<int64_t>(__builtin_amdgcn_readfirstlane(static_cast<int>(v >> 32))) << 32) | lo;
+}
 
 // Memory that no kernel of the call writes: a read at a shared place is a scalar one, and is not
 // counted with the loads of codes.
@@ -61,7 +66,13 @@ struct Plan {
   int join_rows;     // rows of one at most
 };
 
-// The row block that begins in a workgroup's share and goes on in others', the last of them
+// Units of time: of a step, of one where 16 rows do (measured 5 : 2 of 64 rows, 3 : 2 of 32), of
+// a row block itself. tiles: a step's.
+struct Cost {
+  int tiles, step, step16, block;
+};
+
+// The row block that begins in a worker's share and goes on in others', the last of them
 // `last` (0: there is none).
 struct alignas(32) Cut {
   int last, head, c0, row0, rows;
@@ -75,10 +86,12 @@ struct Args {
   int tiles_per_page;
   uint32_t page_inv;  // 2^32 / tiles_per_page, rounded up
   float scale2;       // scale log2 e
-  int workers, items, per_sequence, step;
+  int workers, items, per_sequence;
+  Cost cost;
   // workspace: first[b] = row blocks before sequence b, before[i] = steps before row block i of
   // one key head, before[n] all of them, seq[i] its sequence; the parts; a workgroup's cut
-  int *count, *first, *before, *seq;
+  int *count, *first, *seq;
+  int64_t* before;
   float *part_o, *part_ml;
   Cut* cut;
 };
@@ -87,11 +100,18 @@ struct Args {
 // of them sees.
 struct Block {
   int b, c0, n, len, row0, rows, lo, hi;
-  // In steps of `tiles` key tiles, one more for what a row block costs besides (its queries, its
-  // place, its output: 2 to 3 us, a step's time. Without it the workers with the shortest sequences
-  // ended last: 96 x 40 heads XX -> YY us).
-  __device__ __forceinline__ int steps(int tiles) const {
-    return 2 + ((hi + kTile - 1) / kTile - lo / kTile + tiles - 1) / tiles;
+  // The time of a row block in units: of each step of g.step key tiles, and of what it takes besides
+  // (its place, its queries, its output: 2 to 4 us, which is two or three steps. Without it the workers
+  // with the shortest sequences ended last, 96 x 40 heads 168 us, not 106).
+  __device__ __forceinline__ int per_step(const Cost& c) const { return rows <= 16 ? c.step16 : c.step; }
+  __device__ __forceinline__ int64_t units(const Cost& c) const {
+    const int steps = ((hi + kTile - 1) / kTile - lo / kTile + c.tiles - 1) / c.tiles;
+    return c.block + static_cast<int64_t>(steps) * per_step(c);
+  }
+  // The first step that begins at unit x or behind it.
+  __device__ __forceinline__ int step_at(int64_t x, const Cost& c) const {
+    const int u = per_step(c);
+    return x <= c.block ? 0 : static_cast<int>((x - c.block + u - 1) / u);
   }
 };
 
@@ -119,43 +139,40 @@ __device__ __forceinline__ Block make_block(const Args& g, int b, int rb) {
   return k;
 }
 
-// (steps are fewer than 2^31 but where cu_q does not rise)
-constexpr int kMostSteps = 0x7FFFFFFF;
-__device__ __forceinline__ int held(int a, int b, int most) {
-  return static_cast<int>(min(static_cast<uint32_t>(a) + static_cast<uint32_t>(b), static_cast<uint32_t>(most)));
-}
-__device__ __forceinline__ int wave_scan(int v, int most) {
+template <typename V>
+__device__ __forceinline__ V wave_scan(V v, V most) {
   const int lane = threadIdx.x & 63;
   v = min(v, most);
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
-    const int o = __shfl_up(v, d);
-    if (lane >= d) v = held(v, o, most);
+    const V o = __shfl_up(v, d);
+    if (lane >= d) v = min(v + o, most);
   }
   return v;
 }
 
-// Inclusive sum of v over the workgroup's threads, all the sum, both held at `most`. part: one
-// int a wave.
-template <int WAVES>
-__device__ __forceinline__ int block_scan(int v, int* part, int& all, int most) {
+// Inclusive sum of v over the workgroup's threads, all the sum, both held at `most` (below 2^30 where
+// V is int). part: one place a wave.
+template <int WAVES, typename V>
+__device__ __forceinline__ V block_scan(V v, V* part, V& all, V most) {
   const int wave = threadIdx.x >> 6;
   v = wave_scan(v, most);
   __syncthreads();
   if ((threadIdx.x & 63) == 63) part[wave] = v;
   __syncthreads();
-  int before = 0;
+  V before = 0;
   all = 0;
 #pragma unroll
   for (int w = 0; w < WAVES; ++w) {
-    before = held(before, w < wave ? part[w] : 0, most);
-    all = held(all, part[w], most);
+    before = min(before + (w < wave ? part[w] : V(0)), most);
+    all = min(all + part[w], most);
   }
-  return held(v, before, most);
+  return min(v + before, most);
 }
 
 // The number of entries of the rising list at[0 .. n) that are <= x, less one.
-__device__ __forceinline__ int place_of(const int* at, int n, int64_t x, int64_t times) {
+template <typename V>
+__device__ __forceinline__ int place_of(const V* at, int n, int64_t x, int64_t times) {
   int lo = 0, hi = n;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
@@ -165,19 +182,23 @@ __device__ __forceinline__ int place_of(const int* at, int n, int64_t x, int64_t
   return lo;
 }
 
-// Workgroup w's share begins at step_of(w) of all steps; the workgroup that has step x.
-__device__ __forceinline__ int64_t step_of(int w, int64_t steps, int wgs) { return w * steps / wgs; }
-__device__ __forceinline__ int wg_of(int64_t x, int64_t steps, int wgs) {
-  return static_cast<int>(((x + 1) * wgs - 1) / steps);
+// Worker w's share begins at unit share_of(w) of all units; the worker that has unit x. (Units are
+// fewer than 2^36 5 LN_KV4_MAX_HEADS and workers than 2^13: products stay below 2^62.)
+__device__ __forceinline__ int64_t share_of(int w, int64_t units, int workers) { return w * units / workers; }
+__device__ __forceinline__ int worker_of(int64_t x, int64_t units, int workers) {
+  return static_cast<int>(((x + 1) * workers - 1) / units);
 }
-__device__ __forceinline__ int sharing(int64_t steps, int wgs) {
-  return static_cast<int>(min(static_cast<int64_t>(wgs), steps));
+__device__ __forceinline__ int sharing(int64_t units, int workers) {
+  return static_cast<int>(min(static_cast<int64_t>(workers), units));
 }
 
-// Row blocks and steps of ragged sequences of any length: one workgroup.
+constexpr int64_t kMostUnits = int64_t(1) << 60;
+
+// Row blocks and their units, of ragged sequences of any length: one workgroup.
 constexpr int kPlanThreads = 1024;
 __global__ __launch_bounds__(kPlanThreads) void kv4_plan_kernel(Args g) {
-  __shared__ int part[kPlanThreads / 64];
+  __shared__ int64_t part[kPlanThreads / 64];
+  int* counts = reinterpret_cast<int*>(part);
   const int tid = threadIdx.x;
   int items = 0, all;
   for (int b0 = 0; b0 < g.a.B; b0 += kPlanThreads) {
@@ -185,23 +206,24 @@ __global__ __launch_bounds__(kPlanThreads) void kv4_plan_kernel(Args g) {
     int c0, n = 0;
     if (b < g.a.B) seq_rows(g.a, b, c0, n);
     const int mine = (n * g.heads + g.rows - 1) / g.rows;
-    const int upto = block_scan<kPlanThreads / 64>(mine, part, all, g.items);
+    const int upto = block_scan<kPlanThreads / 64>(mine, counts, all, g.items);
     if (b < g.a.B) g.first[b] = min(items + max(upto - mine, 0), g.items);
-    items = held(items, all, g.items);  // (more only if cu_q does not rise)
+    items = min(items + all, g.items);  // (more only if cu_q does not rise)
   }
   __threadfence_block();
   __syncthreads();
-  int steps = 0;
+  int64_t units = 0, sum;
   for (int i0 = 0; i0 < items; i0 += kPlanThreads) {
     const int i = i0 + tid;
-    int mine = 0, b = 0;
+    int64_t mine = 0;
+    int b = 0;
     if (i < items) {
       b = place_of(g.first, g.a.B, i, 1);
-      mine = make_block(g, b, i - g.first[b]).steps(g.step);
+      mine = make_block(g, b, i - g.first[b]).units(g.cost);
     }
-    const int upto = held(steps, block_scan<kPlanThreads / 64>(mine, part, all, kMostSteps), kMostSteps);
+    const int64_t upto = units + block_scan<kPlanThreads / 64>(mine, part, sum, kMostUnits);
     if (i < items) g.before[i + 1] = upto, g.seq[i] = b;
-    steps = held(steps, all, kMostSteps);
+    units += sum;
   }
   if (tid == 0) g.before[0] = 0, *g.count = items;
 }
@@ -246,8 +268,10 @@ struct Wave {
   int all_lo, all_hi;       // the keys that every row sees
   f32x4_t o[NQ][C][2];
   f32x4_t z[NQ][NZ];        // sum of the rounded p s, four groups in turn in a result's rows
-  float mid[NQ][NG], m[NQ], l[NQ];
-  float x[NQ][2][4];        // a tile's scores
+  float mid[NQ][NG], l[NQ];
+  float m[NQ];              // what is subtracted of scores
+  float bar[NQ];            // the score that raises it
+  float x[NQ][2][4];        // a tile's scores, m subtracted
 
   __device__ __forceinline__ void begin(const Args& g, const Block& k, int h) {
     const int lane = threadIdx.x & 63, col = lane & 15, seg = lane >> 4;
@@ -280,8 +304,8 @@ struct Wave {
       for (int i = 0; i < NZ; ++i) z[t][i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int c = 0; c < C; ++c) o[t][c][0] = o[t][c][1] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-      m[t] = kLowest;
-      l[t] = 0.f;
+      m[t] = l[t] = 0.f;
+      bar[t] = kLowest;
     }
   }
 
@@ -366,7 +390,7 @@ struct Wave {
         for (int t = 0; t < NT; ++t)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float b = i == 0 ? least[e] * q_sum[t][i] : __builtin_fmaf(least[e], q_sum[t][i], x[t][s][e]);
+            const float b = __builtin_fmaf(least[e], q_sum[t][i], i == 0 ? -m[t] : x[t][s][e]);
             x[t][s][e] = __builtin_fmaf(step[e], acc[t][e], b);
           }
       }
@@ -402,11 +426,18 @@ struct Wave {
       float top = x[t][0][0];
 #pragma unroll
       for (int e = 1; e < 8; ++e) top = fmaxf(top, x[t][e >> 2][e & 3]);
-      if (__any(top > m[t] + 8.f)) {
+      if (__any(top > bar[t])) {
         top = fmaxf(top, __shfl_xor(top, 16));
         top = fmaxf(top, __shfl_xor(top, 32));
-        const float now = fmaxf(m[t], top), f = __builtin_amdgcn_exp2f(m[t] - now);
-        m[t] = now;
+        // what is subtracted rises by the tile's largest score where that is positive; of a
+        // query's first keys (its sums are 0) it goes to their largest, which may lie far below 0
+        const bool new_query = bar[t] != kBar;
+        const float was = m[t];
+        m[t] += new_query ? (top < kLowest ? 0.f : top) : fmaxf(top, 0.f);
+        bar[t] = new_query && top < kLowest ? kLowest : kBar;
+        const float rise = m[t] - was, f = new_query ? 1.f : __builtin_amdgcn_exp2f(-rise);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[t][e >> 2][e & 3] -= rise;
         l[t] *= f;
 #pragma unroll
         for (int i = 0; i < NG; ++i) mid[t][i] *= f;
@@ -422,7 +453,7 @@ struct Wave {
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         float& v = x[t][e >> 2][e & 3];
-        v = __builtin_amdgcn_exp2f(v - m[t]);
+        v = __builtin_amdgcn_exp2f(v);
         l[t] += v;
       }
     }
@@ -524,6 +555,7 @@ struct Wave {
   __device__ __forceinline__ void finish() {
 #pragma unroll
     for (int t = 0; t < NQ; ++t) {
+      if (bar[t] != kBar) m[t] = kLowest;
       l[t] += __shfl_xor(l[t], 16);
       l[t] += __shfl_xor(l[t], 32);
 #pragma unroll
@@ -585,23 +617,23 @@ __global__ __launch_bounds__(kThreads, waves_of(D, G, NQ, SOLO)) void kv4_attent
   constexpr int C = D / 32, kStep = SOLO ? 1 : kWaves;
   __shared__ Joined<SOLO ? 0 : D> joined;
   __shared__ Scales<W::NG> scales[kWaves];
-  __shared__ int listed[kListed + 1];
-  __shared__ int part[kWaves];
+  __shared__ int64_t listed[kListed + 1];
+  __shared__ int64_t part[kWaves];
   const int tid = threadIdx.x, wave = uniform(tid >> 6), lane = tid & 63;
   const int col = lane & 15, seg = lane >> 4, n_kv = g.c.n_kv;
 
-  // the steps before every row block
+  // the units before every row block
   int items;
-  const int* before;
+  const int64_t* before;
   if (g.per_sequence) {
     items = g.a.B;
-    int steps = 0, all;
+    int64_t units = 0, all;
     for (int b0 = 0; b0 < items; b0 += kThreads) {
       const int b = b0 + tid;
-      const int mine = b < items ? make_block(g, b, 0).steps(g.step) : 0;
-      const int upto = held(steps, block_scan<kWaves>(mine, part, all, kMostSteps), kMostSteps);
+      const int64_t mine = b < items ? make_block(g, b, 0).units(g.cost) : 0;
+      const int64_t upto = units + block_scan<kWaves>(mine, part, all, kMostUnits);
       if (b < items) listed[b + 1] = upto;
-      steps = held(steps, all, kMostSteps);
+      units += all;
     }
     if (tid == 0) listed[0] = 0;
     __syncthreads();
@@ -610,36 +642,35 @@ __global__ __launch_bounds__(kThreads, waves_of(D, G, NQ, SOLO)) void kv4_attent
     items = *(Const)g.count;
     before = g.before;
   }
-  const int64_t steps = static_cast<int64_t>(uniform(before[items])) * n_kv;
-  const int workers = sharing(steps, g.workers), me = SOLO ? kWaves * blockIdx.x + wave : blockIdx.x;
+  const int64_t units = uniform(before[items]) * n_kv;
+  const int workers = sharing(units, g.workers), me = SOLO ? kWaves * blockIdx.x + wave : blockIdx.x;
   const bool writer = SOLO ? lane == 0 : tid == 0;
   if (me >= workers) {
     if (writer) g.cut[me].last = 0;
     return;
   }
-  const int64_t end = step_of(me + 1, steps, workers), begin = step_of(me, steps, workers);
+  const int64_t end = share_of(me + 1, units, workers);
 
   Cut cut = {0, 0, 0, 0, 0};
-  int64_t at = begin;
+  int64_t at = share_of(me, units, workers);
   int item = uniform(place_of(before, items, at, n_kv));
   while (at < end) {
-    const int base = uniform(before[item]);
-    const int own = uniform(before[item + 1]) - base;  // steps of the row block
-    const int64_t in = at - static_cast<int64_t>(base) * n_kv;
-    const int h = uniform(in >> 32 ? static_cast<int>(in / own)
-                                   : static_cast<int>(static_cast<uint32_t>(in) / static_cast<uint32_t>(own)));
-    const int s0 = uniform(static_cast<int>(in - static_cast<int64_t>(h) * own));
-    const int s1 = uniform(static_cast<int>(min(static_cast<int64_t>(own), s0 + end - at)));
+    const int64_t base = uniform(before[item]), own = uniform(before[item + 1]) - base;  // units of the row block
+    const int64_t in = at - base * n_kv;
+    const int h = uniform((in | own) >> 32 ? static_cast<int>(in / own)
+                                           : static_cast<int>(static_cast<uint32_t>(in) / static_cast<uint32_t>(own)));
+    const int64_t u0 = in - h * own, u1 = min(own, u0 + end - at);
     const int b = g.per_sequence ? item : ((Const)g.seq)[item];
     Block k = make_block(g, b, g.per_sequence ? 0 : item - ((Const)g.first)[b]);
     k.c0 = uniform(k.c0), k.n = uniform(k.n), k.len = uniform(k.len), k.row0 = uniform(k.row0);
     k.rows = uniform(k.rows), k.lo = uniform(k.lo), k.hi = uniform(k.hi);
+    const int s0 = uniform(k.step_at(u0, g.cost)), s1 = uniform(k.step_at(u1, g.cost));
 
     W w;
     w.scales = &scales[wave];
     w.begin(g, k, h);
-    const int t_first = k.lo / kTile + kStep * max(s0 - 2, 0) + (SOLO ? 0 : wave);  // (step 0 has no keys)
-    const int t_end = min((k.hi + kTile - 1) / kTile, k.lo / kTile + kStep * max(s1 - 2, 0));
+    const int t_first = k.lo / kTile + kStep * s0 + (SOLO ? 0 : wave);
+    const int t_end = min((k.hi + kTile - 1) / kTile, k.lo / kTile + kStep * s1);
     if (t_first < t_end) {
       if (NQ > 1 && k.rows <= 16)
         w.template tiles<1, kStep>(g, k, h, t_first, t_end);
@@ -650,8 +681,8 @@ __global__ __launch_bounds__(kThreads, waves_of(D, G, NQ, SOLO)) void kv4_attent
 
     // Whole: y. A part: slot 1 of the worker where the row block begins in its share, 0 where
     // it began before.
-    const bool whole = s0 == 0 && s1 == own;
-    const int64_t slot = 2 * static_cast<int64_t>(me) + (s0 == 0 ? 1 : 0);
+    const bool whole = u0 == 0 && u1 == own;
+    const int64_t slot = 2 * static_cast<int64_t>(me) + (u0 == 0 ? 1 : 0);
     const Out to = {g, k, h, whole, slot};
 #pragma unroll
     for (int t = 0; t < NQ; ++t) {
@@ -695,18 +726,18 @@ __global__ __launch_bounds__(kThreads, waves_of(D, G, NQ, SOLO)) void kv4_attent
         }
       }
     }
-    if (s0 == 0 && s1 < own) cut = {wg_of(at + own - 1, steps, workers), h, k.c0, k.row0, k.rows};
-    at += s1 - s0;
-    if (s1 == own && h == n_kv - 1) ++item;
+    if (u0 == 0 && u1 < own) cut = {worker_of(at + own - 1, units, workers), h, k.c0, k.row0, k.rows};
+    at += u1 - u0;
+    if (u1 == own && h == n_kv - 1) ++item;
   }
   if (writer) g.cut[me] = cut;
 }
 
-// Joins the parts of the row blocks that were cut, a workgroup to a worker's cut (and every n-th
-// of its rows). Its threads in groups of D / 4: kGroups / rows_at of them to every n-th part of
-// one row, rows_at rows at a time.
+// Joins the parts of the row blocks that were cut, a few workgroups to a worker's cut. Threads in
+// groups of D / 4 have a row each where the parts are few (some workers' shares), or every n-th part
+// of one row, four parts' loads in flight.
 template <int D>
-__global__ __launch_bounds__(kThreads) void kv4_join_kernel(Args g, int rows_at) {
+__global__ __launch_bounds__(kThreads) void kv4_join_kernel(Args g) {
   constexpr int kLanes = D / 4, kGroups = kThreads / kLanes;
   __shared__ float4 sum[kGroups][kLanes];
   __shared__ float top[kGroups], all[kGroups];
@@ -715,32 +746,49 @@ __global__ __launch_bounds__(kThreads) void kv4_join_kernel(Args g, int rows_at)
   const int w1 = k.last, h = k.head;
   if (w1 == 0) return;
 
+  const int rows_at = w1 - w0 < 4 ? kGroups : 1;
   const int grp = threadIdx.x / kLanes, d = threadIdx.x % kLanes * 4;
   const int own = grp % rows_at, turn = grp / rows_at, turns = kGroups / rows_at;
   for (int row0 = blockIdx.y * rows_at; row0 < k.rows; row0 += gridDim.y * rows_at) {
-    const int row = row0 + own;
+    const int row = row0 + own, from = min(row, k.rows - 1);
     float m = kLowest, l = 0.f;
     float4 o = {0.f, 0.f, 0.f, 0.f};
-    if (row < k.rows) {
-      for (int w = w0 + turn; w <= w1; w += turns) {
-        const int64_t at = (2 * static_cast<int64_t>(w) + (w == w0 ? 1 : 0)) * g.rows + row;
-        const float2 ml = *reinterpret_cast<const float2*>(g.part_ml + at * 2);
-        const float4 p = *reinterpret_cast<const float4*>(g.part_o + at * D + d);
-        const float now = fmaxf(m, ml.x), f = __builtin_amdgcn_exp2f(m - now), e = __builtin_amdgcn_exp2f(ml.x - now);
-        m = now;
-        l = l * f + ml.y * e;
-        o.x = o.x * f + p.x * e, o.y = o.y * f + p.y * e, o.z = o.z * f + p.z * e, o.w = o.w * f + p.w * e;
+    for (int w = w0 + turn; w <= w1; w += 4 * turns) {
+      float2 ml[4];
+      float4 p[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int v = min(w + i * turns, w1);
+        const int64_t at = (2 * static_cast<int64_t>(v) + (v == w0 ? 1 : 0)) * g.rows + from;
+        ml[i] = *reinterpret_cast<const float2*>(g.part_ml + at * 2);
+        p[i] = *reinterpret_cast<const float4*>(g.part_o + at * D + d);
+      }
+      float now = m;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (w + i * turns > w1) ml[i] = float2{kLowest, 0.f}, p[i] = float4{0.f, 0.f, 0.f, 0.f};
+        now = fmaxf(now, ml[i].x);
+      }
+      const float f = __builtin_amdgcn_exp2f(m - now);
+      m = now;
+      l *= f;
+      o.x *= f, o.y *= f, o.z *= f, o.w *= f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float e = __builtin_amdgcn_exp2f(ml[i].x - now);
+        l += ml[i].y * e;
+        o.x += p[i].x * e, o.y += p[i].y * e, o.z += p[i].z * e, o.w += p[i].w * e;
       }
     }
     if (turns > 1) {
       sum[grp][d / 4] = o;
       if (d == 0) top[grp] = m, all[grp] = l;
       __syncthreads();
-      for (int v = own; v < kGroups; v += rows_at) m = fmaxf(m, top[v]);
-      l = 0.f;
-      o = float4{0.f, 0.f, 0.f, 0.f};
       if (turn == 0) {
-        for (int v = own; v < kGroups; v += rows_at) {
+        for (int v = 0; v < kGroups; ++v) m = fmaxf(m, top[v]);
+        l = 0.f;
+        o = float4{0.f, 0.f, 0.f, 0.f};
+        for (int v = 0; v < kGroups; ++v) {
           const float e = __builtin_amdgcn_exp2f(top[v] - m);
           const float4 p = sum[v][d / 4];
           l += all[v] * e;
@@ -789,7 +837,7 @@ struct Space {
     };
     count = take(4);
     first = take(static_cast<size_t>(B) * 4);
-    before = take((static_cast<size_t>(p.items) + 1) * 4);
+    before = take((static_cast<size_t>(p.items) + 1) * 8);
     seq = take(static_cast<size_t>(p.items) * 4);
     part_o = take(rows * head_dim * 4);
     part_ml = take(rows * 8);
@@ -815,10 +863,8 @@ void launch(const Args& g, const Plan& p, hipStream_t stream) {
     run(std::integral_constant<int, 2>{});
   else
     run(std::integral_constant<int, 4>{});
-  // Few parts of each row block: a group of threads a row. Many: all of them to one row.
-  const int rows_at = p.solo ? kThreads / (D / 4) : 1;
-  const dim3 grid(static_cast<unsigned>(p.workers), static_cast<unsigned>(p.solo ? 1 : p.join_rows));
-  kv4_join_kernel<D><<<grid, kThreads, 0, stream>>>(g, rows_at);
+  const dim3 grid(static_cast<unsigned>(p.workers), static_cast<unsigned>(p.solo ? 1 : std::min(p.join_rows, 8)));
+  kv4_join_kernel<D><<<grid, kThreads, 0, stream>>>(g);
 }
 
 template <int D>
@@ -846,6 +892,7 @@ hipError_t launch_kv4_attention(const Kv4Attention& a, const ln_kv4_cache& c, vo
   auto* ws = static_cast<uint8_t*>(workspace);
   Args g;
   g.a = a;
+  if (g.a.window >= 1 << 30) g.a.window = 0;  // (no sequence is longer)
   g.c = c;
   g.heads = a.n_q / c.n_kv;
   g.rows = 16 * p.nq;
@@ -855,10 +902,11 @@ hipError_t launch_kv4_attention(const Kv4Attention& a, const ln_kv4_cache& c, vo
   g.workers = p.workers;
   g.items = p.items;
   g.per_sequence = p.per_sequence;
-  g.step = p.solo ? 1 : kWaves;
+  const int tiles = p.solo ? 1 : kWaves;
+  g.cost = p.nq == 1 ? Cost{tiles, 1, 1, 2} : p.nq == 2 ? Cost{tiles, 3, 2, 6} : Cost{tiles, 5, 2, 15};
   g.count = reinterpret_cast<int*>(ws + sp.count);
   g.first = reinterpret_cast<int*>(ws + sp.first);
-  g.before = reinterpret_cast<int*>(ws + sp.before);
+  g.before = reinterpret_cast<int64_t*>(ws + sp.before);
   g.seq = reinterpret_cast<int*>(ws + sp.seq);
   g.part_o = reinterpret_cast<float*>(ws + sp.part_o);
   g.part_ml = reinterpret_cast<float*>(ws + sp.part_ml);

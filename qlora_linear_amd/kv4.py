@@ -17,6 +17,7 @@ writes the cache in place: calls on one cache from several streams are ordered b
 from __future__ import annotations
 
 import ctypes
+import functools
 from array import array
 
 import torch
@@ -174,6 +175,7 @@ def kv4_read(cache, slots, dtype=torch.bfloat16):
     return k, v
 
 
+@functools.lru_cache(maxsize=256)  # (a pure function of sizes, which a decode loop repeats)
 def kv4_attention_workspace_bytes(T: int, B: int, n_q: int, n_kv: int, head_dim: int, max_q: int, max_pages: int,
                                   page_size: int) -> int:
     return int(library().kv4_attention_workspace_bytes(T, B, n_q, n_kv, head_dim, max_q, max_pages, page_size))

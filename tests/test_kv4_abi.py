@@ -110,7 +110,7 @@ def test_attention_refusals(lib):
     assert attend(lib, n_q=3) == attend(lib, n_q=1026, qs=1 << 20) == attend(lib, T=4) == attend(lib, qs=255) == ESHAPE
     assert attend(lib, T=1 << 24, B=1, cu=at(9)) == attend(lib, B=1 << 20, T=1 << 20) == ESHAPE
     assert attend(lib, T=1 << 22, n_q=512, qs=1 << 20, B=1, cu=at(9)) == attend(lib, pages=(1 << 25) + 1) == ESHAPE
-    assert attend(lib, pages=1 << 25, T=1 << 16, B=1 << 16) == ESHAPE
+    assert attend(lib, pages=1 << 25, T=1 << 19, B=1 << 19) == ESHAPE
     assert attend(lib, ws=None) == attend(lib, nb=0) == EWORKSPACE
     need = lib.kv4_attention_workspace_bytes(3, 3, 4, 2, 64, 1, 5, 32)
     assert attend(lib, nb=need - 1) == EWORKSPACE and attend(lib, ws=at(5) + 16) == EALIGN
