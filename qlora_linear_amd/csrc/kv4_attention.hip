@@ -39,9 +39,9 @@ constexpr int kListed = 512;         // sequences whose steps are summed in LDS
 
 // 16-row tiles of a row block at most, and the waves a SIMD that the registers are cut for
 // (workgroups a CU, then): as many as need no scratch memory.
-constexpr int most_nq(int D) { return D == 64 ? 4 : D == 128 ? 2 : 1; }
+constexpr int most_nq(int D, int G) { return D == 64 ? (G == 64 ? 4 : 2) : D == 128 ? 2 : 1; }
 constexpr int waves_of(int D, int G, int NQ, bool SOLO) {
-  if (D == 64) return NQ == 1 ? 4 : NQ == 2 ? 3 : 2;
+  if (D == 64) return NQ == 1 ? 4 : NQ == 2 && (SOLO || G == 64) ? 3 : 2;
   if (D == 128 && NQ == 1) return 3;
   return 2;
 }
@@ -64,6 +64,8 @@ struct Plan {
   bool per_sequence; // one row block a sequence: workgroups sum the steps themselves
   int nq;            // 16-row tiles of a row block
   int join_rows;     // rows of one at most
+  bool by_head;      // cuts are listed by row block and head, not by worker
+  int cuts;
 };
 
 // Units of time: of a step, of one where 16 rows do (measured 5 : 2 of 64 rows, 3 : 2 of 32), of
@@ -72,10 +74,10 @@ struct Cost {
   int tiles, step, step16, block;
 };
 
-// The row block that begins in a worker's share and goes on in others', the last of them
-// `last` (0: there is none).
+// A row block of a head that begins in worker `begun`'s share and goes on in others', the last of
+// them `last` (0: there is none).
 struct alignas(32) Cut {
-  int last, head, c0, row0, rows;
+  int begun, last, head, c0, row0, rows;
 };
 
 struct Args {
@@ -93,7 +95,8 @@ struct Args {
   int *count, *first, *seq;
   int64_t* before;
   float *part_o, *part_ml;
-  Cut* cut;
+  Cut* cut;      // of every worker, of which one at most begins what it does not end; or (by_head) of every
+  int by_head;   // row block and head, where those are fewer
 };
 
 // A row block: rows [row0, row0 + rows) of a sequence's n_b heads rows, keys [lo, hi) that any
@@ -615,8 +618,12 @@ template <int D, int G, int NQ, bool SOLO>
 __global__ __launch_bounds__(kThreads, waves_of(D, G, NQ, SOLO)) void kv4_attention_kernel(Args g) {
   typedef Wave<D, G, NQ> W;
   constexpr int C = D / 32, kStep = SOLO ? 1 : kWaves;
-  __shared__ Joined<SOLO ? 0 : D> joined;
-  __shared__ Scales<W::NG> scales[kWaves];
+  __shared__ union {
+    Scales<W::NG> scales[kWaves];   // in the loop over tiles
+    Joined<SOLO ? 0 : D> joined;    // after it
+  } space;
+  auto& scales = space.scales;
+  auto& joined = space.joined;
   __shared__ int64_t listed[kListed + 1];
   __shared__ int64_t part[kWaves];
   const int tid = threadIdx.x, wave = uniform(tid >> 6), lane = tid & 63;
@@ -646,12 +653,12 @@ __global__ __launch_bounds__(kThreads, waves_of(D, G, NQ, SOLO)) void kv4_attent
   const int workers = sharing(units, g.workers), me = SOLO ? kWaves * blockIdx.x + wave : blockIdx.x;
   const bool writer = SOLO ? lane == 0 : tid == 0;
   if (me >= workers) {
-    if (writer) g.cut[me].last = 0;
+    if (writer && !g.by_head) g.cut[me].last = 0;
     return;
   }
   const int64_t end = share_of(me + 1, units, workers);
 
-  Cut cut = {0, 0, 0, 0, 0};
+  Cut cut = {0, 0, 0, 0, 0, 0};
   int64_t at = share_of(me, units, workers);
   int item = uniform(place_of(before, items, at, n_kv));
   while (at < end) {
@@ -726,14 +733,19 @@ __global__ __launch_bounds__(kThreads, waves_of(D, G, NQ, SOLO)) void kv4_attent
         }
       }
     }
-    if (u0 == 0 && u1 < own) cut = {worker_of(at + own - 1, units, workers), h, k.c0, k.row0, k.rows};
+    if constexpr (!SOLO) __syncthreads();
+    if (u0 == 0) {
+      const bool goes_on = u1 < own;
+      if (goes_on) cut = {me, worker_of(at + own - 1, units, workers), h, k.c0, k.row0, k.rows};
+      if (g.by_head && writer) g.cut[static_cast<int64_t>(item) * n_kv + h] = goes_on ? cut : Cut{0, 0, 0, 0, 0, 0};
+    }
     at += u1 - u0;
     if (u1 == own && h == n_kv - 1) ++item;
   }
-  if (writer) g.cut[me] = cut;
+  if (writer && !g.by_head) g.cut[me] = cut;
 }
 
-// Joins the parts of the row blocks that were cut, a few workgroups to a worker's cut. Threads in
+// Joins the parts of the row blocks that were cut, a few workgroups to a cut. Threads in
 // groups of D / 4 have a row each where the parts are few (some workers' shares), or every n-th part
 // of one row, four parts' loads in flight.
 template <int D>
@@ -741,9 +753,8 @@ __global__ __launch_bounds__(kThreads) void kv4_join_kernel(Args g) {
   constexpr int kLanes = D / 4, kGroups = kThreads / kLanes;
   __shared__ float4 sum[kGroups][kLanes];
   __shared__ float top[kGroups], all[kGroups];
-  const int w0 = blockIdx.x;
-  const Cut k = g.cut[w0];
-  const int w1 = k.last, h = k.head;
+  const Cut k = g.cut[blockIdx.x];
+  const int w0 = k.begun, w1 = k.last, h = k.head;
   if (w1 == 0) return;
 
   const int rows_at = w1 - w0 < 4 ? kGroups : 1;
@@ -814,12 +825,16 @@ Plan plan_of(int64_t T, int64_t B, int n_q, int n_kv, int head_dim, int max_q, i
   const int64_t heads = n_q / n_kv;
   const int64_t most = max_q > 0 ? max_q * heads : (T * heads + B - 1) / B;
   Plan p;
-  p.nq = std::min(most <= 16 ? 1 : most <= 32 ? 2 : 4, most_nq(head_dim));
+  p.nq = std::min(most <= 16 ? 1 : most <= 32 ? 2 : 4, most_nq(head_dim, group));
   p.per_sequence = max_q > 0 && max_q * heads <= 16 * p.nq && B <= kListed;
   p.items = static_cast<int>(p.per_sequence ? B : T * heads / (16 * p.nq) + std::min(T, B));
   p.join_rows = static_cast<int>(max_q > 0 ? std::min<int64_t>(most, 16 * p.nq) : 16 * p.nq);
   p.solo = solo_of(p.items, n_kv);
+  // (of a ragged batch the row blocks are known to the GPU only)
+  p.by_head = p.per_sequence;
   p.workers = 256 * waves_of(head_dim, group, p.nq, p.solo) * (p.solo ? kWaves : 1);
+  if (p.by_head && static_cast<int64_t>(p.items) * n_kv >= p.workers) p.by_head = false;
+  p.cuts = p.by_head ? p.items * n_kv : p.workers;
   return p;
 }
 
@@ -841,7 +856,7 @@ struct Space {
     seq = take(static_cast<size_t>(p.items) * 4);
     part_o = take(rows * head_dim * 4);
     part_ml = take(rows * 8);
-    cut = take(static_cast<size_t>(p.workers) * sizeof(Cut));
+    cut = take(static_cast<size_t>(p.cuts) * sizeof(Cut));
     all = at;
   }
 };
@@ -850,7 +865,7 @@ template <int D, int G>
 void launch(const Args& g, const Plan& p, hipStream_t stream) {
   auto run = [&](auto nq) {
     constexpr int NQ = decltype(nq)::value;
-    if constexpr (NQ <= most_nq(D)) {
+    if constexpr (NQ <= most_nq(D, G)) {
       if (p.solo)
         kv4_attention_kernel<D, G, NQ, true><<<p.workers / kWaves, kThreads, 0, stream>>>(g);
       else
@@ -863,7 +878,8 @@ void launch(const Args& g, const Plan& p, hipStream_t stream) {
     run(std::integral_constant<int, 2>{});
   else
     run(std::integral_constant<int, 4>{});
-  const dim3 grid(static_cast<unsigned>(p.workers), static_cast<unsigned>(p.solo ? 1 : std::min(p.join_rows, 8)));
+  const int at_once = p.solo ? kThreads / (D / 4) : 1;  // rows of a workgroup
+  const dim3 grid(static_cast<unsigned>(p.cuts), static_cast<unsigned>(std::min((p.join_rows + at_once - 1) / at_once, 8)));
   kv4_join_kernel<D><<<grid, kThreads, 0, stream>>>(g);
 }
 
@@ -900,6 +916,7 @@ hipError_t launch_kv4_attention(const Kv4Attention& a, const ln_kv4_cache& c, vo
   g.page_inv = static_cast<uint32_t>(((uint64_t(1) << 32) + g.tiles_per_page - 1) / g.tiles_per_page);
   g.scale2 = a.scale * 1.4426950408889634f;
   g.workers = p.workers;
+  g.by_head = p.by_head;
   g.items = p.items;
   g.per_sequence = p.per_sequence;
   const int tiles = p.solo ? 1 : kWaves;
