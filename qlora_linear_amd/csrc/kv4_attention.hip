@@ -61,7 +61,7 @@ struct Plan {
   bool solo;         // the workers that share the steps are waves, not workgroups
   int workers;
   int items;         // row blocks at most
-  bool per_sequence; // one row block a sequence: workgroups sum the steps themselves
+  int in_seq;        // row blocks of a sequence, where workgroups sum the units themselves; else 0
   int nq;            // 16-row tiles of a row block
   int join_rows;     // rows of one at most
   bool by_head;      // cuts are listed by row block and head, not by worker
@@ -88,7 +88,8 @@ struct Args {
   int tiles_per_page;
   uint32_t page_inv;  // 2^32 / tiles_per_page, rounded up
   float scale2;       // scale log2 e
-  int workers, items, per_sequence;
+  int workers, items;
+  int in_seq;         // row blocks of every sequence, which workgroups then list themselves; 0: seq lists them
   Cost cost;
   // workspace: first[b] = row blocks before sequence b, before[i] = steps before row block i of
   // one key head, before[n] all of them, seq[i] its sequence; the parts; a workgroup's cut
@@ -632,14 +633,18 @@ __global__ __launch_bounds__(kThreads, waves_of(D, G, NQ, SOLO)) void kv4_attent
   // the units before every row block
   int items;
   const int64_t* before;
-  if (g.per_sequence) {
-    items = g.a.B;
+  if (g.in_seq != 0) {
+    items = g.a.B * g.in_seq;
     int64_t units = 0, all;
     for (int b0 = 0; b0 < items; b0 += kThreads) {
-      const int b = b0 + tid;
-      const int64_t mine = b < items ? make_block(g, b, 0).units(g.cost) : 0;
+      const int i = b0 + tid;
+      int64_t mine = 0;
+      if (i < items) {
+        const Block k = make_block(g, i / g.in_seq, i % g.in_seq);
+        mine = k.row0 == 0 || k.rows > 0 ? k.units(g.cost) : 0;  // (sequences differ in rows)
+      }
       const int64_t upto = units + block_scan<kWaves>(mine, part, all, kMostUnits);
-      if (b < items) listed[b + 1] = upto;
+      if (i < items) listed[i + 1] = upto;
       units += all;
     }
     if (tid == 0) listed[0] = 0;
@@ -663,12 +668,16 @@ __global__ __launch_bounds__(kThreads, waves_of(D, G, NQ, SOLO)) void kv4_attent
   int item = uniform(place_of(before, items, at, n_kv));
   while (at < end) {
     const int64_t base = uniform(before[item]), own = uniform(before[item + 1]) - base;  // units of the row block
+    if (own == 0) {
+      ++item;
+      continue;
+    }
     const int64_t in = at - base * n_kv;
     const int h = uniform((in | own) >> 32 ? static_cast<int>(in / own)
                                            : static_cast<int>(static_cast<uint32_t>(in) / static_cast<uint32_t>(own)));
     const int64_t u0 = in - h * own, u1 = min(own, u0 + end - at);
-    const int b = g.per_sequence ? item : ((Const)g.seq)[item];
-    Block k = make_block(g, b, g.per_sequence ? 0 : item - ((Const)g.first)[b]);
+    const int b = g.in_seq != 0 ? item / g.in_seq : ((Const)g.seq)[item];
+    Block k = make_block(g, b, item - (g.in_seq != 0 ? b * g.in_seq : ((Const)g.first)[b]));
     k.c0 = uniform(k.c0), k.n = uniform(k.n), k.len = uniform(k.len), k.row0 = uniform(k.row0);
     k.rows = uniform(k.rows), k.lo = uniform(k.lo), k.hi = uniform(k.hi);
     const int s0 = uniform(k.step_at(u0, g.cost)), s1 = uniform(k.step_at(u1, g.cost));
@@ -826,12 +835,13 @@ Plan plan_of(int64_t T, int64_t B, int n_q, int n_kv, int head_dim, int max_q, i
   const int64_t most = max_q > 0 ? max_q * heads : (T * heads + B - 1) / B;
   Plan p;
   p.nq = std::min(most <= 16 ? 1 : most <= 32 ? 2 : 4, most_nq(head_dim, group));
-  p.per_sequence = max_q > 0 && max_q * heads <= 16 * p.nq && B <= kListed;
-  p.items = static_cast<int>(p.per_sequence ? B : T * heads / (16 * p.nq) + std::min(T, B));
+  const int64_t blocks = (most + 16 * p.nq - 1) / (16 * p.nq);
+  p.in_seq = max_q > 0 && B * blocks <= kListed ? static_cast<int>(blocks) : 0;
+  p.items = static_cast<int>(p.in_seq != 0 ? B * blocks : T * heads / (16 * p.nq) + std::min(T, B));
   p.join_rows = static_cast<int>(max_q > 0 ? std::min<int64_t>(most, 16 * p.nq) : 16 * p.nq);
   p.solo = solo_of(p.items, n_kv);
   // (of a ragged batch the row blocks are known to the GPU only)
-  p.by_head = p.per_sequence;
+  p.by_head = p.in_seq == 1;
   p.workers = 256 * waves_of(head_dim, group, p.nq, p.solo) * (p.solo ? kWaves : 1);
   if (p.by_head && static_cast<int64_t>(p.items) * n_kv >= p.workers) p.by_head = false;
   p.cuts = p.by_head ? p.items * n_kv : p.workers;
@@ -918,7 +928,7 @@ hipError_t launch_kv4_attention(const Kv4Attention& a, const ln_kv4_cache& c, vo
   g.workers = p.workers;
   g.by_head = p.by_head;
   g.items = p.items;
-  g.per_sequence = p.per_sequence;
+  g.in_seq = p.in_seq;
   const int tiles = p.solo ? 1 : kWaves;
   g.cost = p.nq == 1 ? Cost{tiles, 1, 1, 2} : p.nq == 2 ? Cost{tiles, 3, 2, 6} : Cost{tiles, 5, 2, 15};
   g.count = reinterpret_cast<int*>(ws + sp.count);
@@ -928,7 +938,7 @@ hipError_t launch_kv4_attention(const Kv4Attention& a, const ln_kv4_cache& c, vo
   g.part_o = reinterpret_cast<float*>(ws + sp.part_o);
   g.part_ml = reinterpret_cast<float*>(ws + sp.part_ml);
   g.cut = reinterpret_cast<Cut*>(ws + sp.cut);
-  if (!p.per_sequence) kv4_plan_kernel<<<1, kPlanThreads, 0, stream>>>(g);
+  if (p.in_seq == 0) kv4_plan_kernel<<<1, kPlanThreads, 0, stream>>>(g);
   if (c.head_dim == 64)
     launch_group<64>(g, p, stream);
   else if (c.head_dim == 128)
