@@ -123,7 +123,7 @@ int kv4_read(int64_t T, const int64_t* slots, const ln_kv4_cache* cache, int out
 size_t kv4_attention_workspace_bytes(int64_t T, int64_t B, int32_t n_q, int32_t n_kv, int32_t head_dim, int32_t max_q,
                                      int64_t max_pages, int32_t page_size) {
   if (T == 0 || check_attention(T, B, n_q, n_kv, head_dim, max_q, max_pages, page_size) != LN_OK) return 0;
-  return kv4_attention_bytes(T, B, n_q, n_kv, head_dim, max_q);
+  return kv4_attention_bytes(T, B, n_q, n_kv, head_dim, max_q, max_pages * page_size);
 }
 
 int kv4_attention(int64_t T, int64_t B, int32_t n_q, const uint16_t* q, int64_t q_stride, const int32_t* cu_q,
@@ -144,7 +144,7 @@ int kv4_attention(int64_t T, int64_t B, int32_t n_q, const uint16_t* q, int64_t 
       !aligned16(y) || !aligned16(lse))
     return LN_EALIGN;
   const int32_t bound = cu_q == nullptr ? 1 : max_q;
-  const size_t need = kv4_attention_bytes(T, B, n_q, cache->n_kv, cache->head_dim, bound);
+  const size_t need = kv4_attention_bytes(T, B, n_q, cache->n_kv, cache->head_dim, bound, max_pages * cache->page_size);
   if (workspace == nullptr || workspace_bytes < need) return LN_EWORKSPACE;
   if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return LN_EALIGN;
   const size_t t = static_cast<size_t>(T), b = static_cast<size_t>(B);

@@ -64,6 +64,7 @@ struct Plan {
   int in_seq;        // row blocks of a sequence, where workgroups sum the units themselves; else 0
   int nq;            // 16-row tiles of a row block
   int join_rows;     // rows of one at most
+  bool whole;        // a worker to each row block and head
   bool by_head;      // cuts are listed by row block and head, not by worker
   int cuts;
 };
@@ -89,6 +90,7 @@ struct Args {
   uint32_t page_inv;  // 2^32 / tiles_per_page, rounded up
   float scale2;       // scale log2 e
   int workers, items;
+  int whole;          // a worker to each row block and head, which nothing cuts
   int in_seq;         // row blocks of every sequence, which workgroups then list themselves; 0: seq lists them
   Cost cost;
   // workspace: first[b] = row blocks before sequence b, before[i] = steps before row block i of
@@ -632,8 +634,10 @@ __global__ __launch_bounds__(kThreads, waves_of(D, G, NQ, SOLO)) void kv4_attent
 
   // the units before every row block
   int items;
-  const int64_t* before;
-  if (g.in_seq != 0) {
+  const int64_t* before = nullptr;
+  if (g.whole) {
+    items = g.items;
+  } else if (g.in_seq != 0) {
     items = g.a.B * g.in_seq;
     int64_t units = 0, all;
     for (int b0 = 0; b0 < items; b0 += kThreads) {
@@ -654,7 +658,7 @@ __global__ __launch_bounds__(kThreads, waves_of(D, G, NQ, SOLO)) void kv4_attent
     items = *(Const)g.count;
     before = g.before;
   }
-  const int64_t units = uniform(before[items]) * n_kv;
+  const int64_t units = g.whole ? g.workers : uniform(before[items]) * n_kv;
   const int workers = sharing(units, g.workers), me = SOLO ? kWaves * blockIdx.x + wave : blockIdx.x;
   const bool writer = SOLO ? lane == 0 : tid == 0;
   if (me >= workers) {
@@ -665,9 +669,10 @@ __global__ __launch_bounds__(kThreads, waves_of(D, G, NQ, SOLO)) void kv4_attent
 
   Cut cut = {0, 0, 0, 0, 0, 0};
   int64_t at = share_of(me, units, workers);
-  int item = uniform(place_of(before, items, at, n_kv));
+  int item = g.whole ? me / n_kv : uniform(place_of(before, items, at, n_kv));
   while (at < end) {
-    const int64_t base = uniform(before[item]), own = uniform(before[item + 1]) - base;  // units of the row block
+    const int64_t base = g.whole ? item : uniform(before[item]);
+    const int64_t own = g.whole ? 1 : uniform(before[item + 1]) - base;  // units of the row block
     if (own == 0) {
       ++item;
       continue;
@@ -680,7 +685,7 @@ __global__ __launch_bounds__(kThreads, waves_of(D, G, NQ, SOLO)) void kv4_attent
     Block k = make_block(g, b, item - (g.in_seq != 0 ? b * g.in_seq : ((Const)g.first)[b]));
     k.c0 = uniform(k.c0), k.n = uniform(k.n), k.len = uniform(k.len), k.row0 = uniform(k.row0);
     k.rows = uniform(k.rows), k.lo = uniform(k.lo), k.hi = uniform(k.hi);
-    const int s0 = uniform(k.step_at(u0, g.cost)), s1 = uniform(k.step_at(u1, g.cost));
+    const int s0 = uniform(k.step_at(u0, g.cost)), s1 = g.whole ? 1 << 20 : uniform(k.step_at(u1, g.cost));
 
     W w;
     w.scales = &scales[wave];
@@ -751,7 +756,7 @@ __global__ __launch_bounds__(kThreads, waves_of(D, G, NQ, SOLO)) void kv4_attent
     at += u1 - u0;
     if (u1 == own && h == n_kv - 1) ++item;
   }
-  if (writer && !g.by_head) g.cut[me] = cut;
+  if (writer && !g.by_head && !g.whole) g.cut[me] = cut;
 }
 
 // Joins the parts of the row blocks that were cut, a few workgroups to a cut. Threads in
@@ -830,7 +835,7 @@ __global__ __launch_bounds__(kThreads) void kv4_join_kernel(Args g) {
 bool solo_of(int64_t items, int n_kv) { return items * n_kv >= 1024; }
 
 // Rows of a row block: 16, 32 or 64, as many as a sequence's new tokens fill.
-Plan plan_of(int64_t T, int64_t B, int n_q, int n_kv, int head_dim, int max_q, int group) {
+Plan plan_of(int64_t T, int64_t B, int n_q, int n_kv, int head_dim, int max_q, int64_t max_len, int group) {
   const int64_t heads = n_q / n_kv;
   const int64_t most = max_q > 0 ? max_q * heads : (T * heads + B - 1) / B;
   Plan p;
@@ -840,11 +845,14 @@ Plan plan_of(int64_t T, int64_t B, int n_q, int n_kv, int head_dim, int max_q, i
   p.items = static_cast<int>(p.in_seq != 0 ? B * blocks : T * heads / (16 * p.nq) + std::min(T, B));
   p.join_rows = static_cast<int>(max_q > 0 ? std::min<int64_t>(most, 16 * p.nq) : 16 * p.nq);
   p.solo = solo_of(p.items, n_kv);
-  // (of a ragged batch the row blocks are known to the GPU only)
-  p.by_head = p.in_seq == 1;
+  p.by_head = p.in_seq == 1;  // (the row blocks of others are known to the GPU only)
   p.workers = 256 * waves_of(head_dim, group, p.nq, p.solo) * (p.solo ? kWaves : 1);
   if (p.by_head && static_cast<int64_t>(p.items) * n_kv >= p.workers) p.by_head = false;
   p.cuts = p.by_head ? p.items * n_kv : p.workers;
+  // Up to 512 keys are four tiles a wave, which take no longer than a second launch does (a token
+  // after 500 keys in a call XX us, YY in two launches).
+  p.whole = p.in_seq != 0 && !p.solo && max_len <= 512 && static_cast<int64_t>(p.items) * n_kv <= p.workers;
+  if (p.whole) p.workers = p.items * n_kv, p.by_head = false, p.cuts = 0;
   return p;
 }
 
@@ -853,7 +861,7 @@ size_t up256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
 struct Space {
   size_t count, first, before, seq, part_o, part_ml, cut, all;
   Space(const Plan& p, int64_t B, int head_dim) {
-    const size_t rows = static_cast<size_t>(p.workers) * 2 * 16 * p.nq;
+    const size_t rows = p.whole ? 0 : static_cast<size_t>(p.workers) * 2 * 16 * p.nq;
     size_t at = 0;
     auto take = [&](size_t bytes) {
       const size_t here = at;
@@ -888,6 +896,7 @@ void launch(const Args& g, const Plan& p, hipStream_t stream) {
     run(std::integral_constant<int, 2>{});
   else
     run(std::integral_constant<int, 4>{});
+  if (p.whole) return;
   const int at_once = p.solo ? kThreads / (D / 4) : 1;  // rows of a workgroup
   const dim3 grid(static_cast<unsigned>(p.cuts), static_cast<unsigned>(std::min((p.join_rows + at_once - 1) / at_once, 8)));
   kv4_join_kernel<D><<<grid, kThreads, 0, stream>>>(g);
@@ -905,15 +914,15 @@ void launch_group(const Args& g, const Plan& p, hipStream_t stream) {
 
 }  // namespace
 
-size_t kv4_attention_bytes(int64_t T, int64_t B, int n_q, int n_kv, int head_dim, int max_q) {
+size_t kv4_attention_bytes(int64_t T, int64_t B, int n_q, int n_kv, int head_dim, int max_q, int64_t max_len) {
   size_t most = 0;
   for (int group = 32; group <= 128; group *= 2)
-    most = std::max(most, Space(plan_of(T, B, n_q, n_kv, head_dim, max_q, group), B, head_dim).all);
+    most = std::max(most, Space(plan_of(T, B, n_q, n_kv, head_dim, max_q, max_len, group), B, head_dim).all);
   return most;
 }
 
 hipError_t launch_kv4_attention(const Kv4Attention& a, const ln_kv4_cache& c, void* workspace, hipStream_t stream) {
-  const Plan p = plan_of(a.T, a.B, a.n_q, c.n_kv, c.head_dim, a.max_q, c.group);
+  const Plan p = plan_of(a.T, a.B, a.n_q, c.n_kv, c.head_dim, a.max_q, static_cast<int64_t>(a.max_pages) * c.page_size, c.group);
   const Space sp(p, a.B, c.head_dim);
   auto* ws = static_cast<uint8_t*>(workspace);
   Args g;
@@ -927,6 +936,7 @@ hipError_t launch_kv4_attention(const Kv4Attention& a, const ln_kv4_cache& c, vo
   g.scale2 = a.scale * 1.4426950408889634f;
   g.workers = p.workers;
   g.by_head = p.by_head;
+  g.whole = p.whole;
   g.items = p.items;
   g.in_seq = p.in_seq;
   const int tiles = p.solo ? 1 : kWaves;

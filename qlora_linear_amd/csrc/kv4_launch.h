@@ -39,7 +39,7 @@ struct Kv4Attention {
   uint16_t* y;
   float* lse;
 };
-size_t kv4_attention_bytes(int64_t T, int64_t B, int n_q, int n_kv, int head_dim, int max_q);
+size_t kv4_attention_bytes(int64_t T, int64_t B, int n_q, int n_kv, int head_dim, int max_q, int64_t max_len);
 hipError_t launch_kv4_attention(const Kv4Attention& a, const ln_kv4_cache& c, void* workspace, hipStream_t stream);
 
 }  // namespace lnf4
