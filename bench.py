@@ -21,7 +21,8 @@ cold (after a 1 GiB read), and `small_tokens_headline_projection` the headline
 projection at a few tokens; `medium_tokens` does the same at a few hundred
 tokens (tiled kernels on a grid of 128 x 128 tiles); `merge` times lora_nf4_merge of that
 projection (the 16-bit export, also HBM-bound); `served_projection` the merged weight packed to
-4 bits and multiplied with the norm's 8-bit rows, and the norm forward and backward; `rank_r_gradients` times the backward's
+4 bits and multiplied with the norm's 8-bit rows, and the norm forward and backward; `served_attention` a decode
+step's append to the paged 4-bit cache and its attention, 64 sequences of 4096 keys; `rank_r_gradients` times the backward's
 rank-r step alone (lora_nf4_grad_ab, bound by reading x and dY); `train_step` times the AdamW step of A and B and the
 absmax double quantization; `multi_projection` times Llama-3-8B q/k/v (r = 64, one x) as one
 lora_nf4_fwd_multi + lora_nf4_bwd_multi against separate calls. With --fuse, projections that read the same
@@ -540,6 +541,43 @@ def serve_run(lib, q, torch, d, w, sp, rows=(1, 16), group=128, reps=50):
         T, K, 1, x, res, h, weight.data_ptr(), rstd.data_ptr(), y, dw.data_ptr(), ws.data_ptr(), ws.numel(), sp),
         T * K * 8)
     return out
+
+
+def cache_run(q, torch, B=64, keys=4096, n_q=32, n_kv=8, D=128, group=128, page=64, reps=50):
+    """One layer's cache in a decode step of B sequences of `keys` keys each (Llama-3-8B's heads):
+    kv4_append of a token each with the rotation, and kv4_attention over the cache, HIP events around
+    `reps` back-to-back calls of the binding; bytes of the attention = the sequences' part of the cache + q + y."""
+    pages = B * keys // page
+    cache = q.kv4_cache(pages, n_kv, D, page, group)
+    gen = torch.Generator(device="cuda").manual_seed(7)
+    table = torch.randperm(pages, generator=gen, device="cuda").view(B, -1)
+    qkv = [torch.randn(B, n, D, generator=gen, device="cuda").bfloat16() for n in (n_q, n_kv, n_kv)]
+    angle = torch.arange(keys, device="cuda")[:, None] * 1e4 ** (-torch.arange(0, D, 2, device="cuda") / D)
+    kw = dict(cos=angle.cos(), sin=angle.sin(), positions=torch.full((B,), keys - 1, device="cuda"))
+    fill = torch.randn(keys, n_kv, D, generator=gen, device="cuda").bfloat16()
+    at = torch.arange(keys, device="cuda")
+    for b in range(B):
+        q.kv4_append(None, fill, fill, cache, table[b][at // page] * page + at % page)
+    slots = table[:, -1] * page + page - 1
+    lens, table = torch.full((B,), keys, dtype=torch.int32, device="cuda"), table.int()
+    ws = torch.empty(q.kv4_attention_workspace_bytes(B, B, n_q, n_kv, D, 1, table.shape[1], page), dtype=torch.uint8,
+                     device="cuda")
+    y = torch.empty_like(qkv[0])
+    read = B * keys * 2 * n_kv * (D // 2 + 4 * D // group) + 2 * 2 * B * n_q * D
+    out = {"sequences": B, "keys": keys, "heads": [n_q, n_kv, D], "group": group, "bound": "hbm", "bytes": read}
+    for name, call in (("append", lambda: q.kv4_append(*qkv, cache, slots, **kw)),
+                       ("attention", lambda: q.kv4_attention(qkv[0], cache, table, lens, out=y, workspace=ws))):
+        for _ in range(5):
+            call()
+        e0, e1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        e0.record()
+        for _ in range(reps):
+            call()
+        e1.record()
+        torch.cuda.synchronize()
+        out[name + "_us"] = round(e0.elapsed_time(e1) * 1000.0 / reps, 2)
+    gbs = read / out["attention_us"] / 1e3
+    return dict(out, achieved=round(gbs, 1), peak=PEAK_HBM_GBS, unit="GB/s", frac=round(gbs / PEAK_HBM_GBS, 4))
 
 
 def rank_r_run(lib, q, torch, d, w, sp, reps=50):
@@ -1274,6 +1312,7 @@ def main():
         out["medium_tokens"] = medium_token_run(lib, q, torch, run.projs[run.units[bu][0]], w, args.medium_tokens, sp)
     out["merge"] = merge_run(lib, q, torch, run.projs[run.units[bu][0]], w, sp)
     out["served_projection"] = serve_run(lib, q, torch, run.projs[run.units[bu][0]], w, sp)
+    out["served_attention"] = cache_run(q, torch)
     out["rank_r_gradients"] = rank_r_run(lib, q, torch, run.projs[run.units[bu][0]], w, sp)
     out["train_step"] = train_step_run(lib, q, torch, run.projs[run.units[bu][0]], w, sp)
     progress("small / medium tokens, merge, training step done")

@@ -127,7 +127,7 @@ int kv4_read(int64_t T, const int64_t* slots, const ln_kv4_cache* cache, int out
  *               over workgroups (float32 sums of the parts, joined in a fixed order: the result
  *               does not depend on the run); two calls that may run at the same time need
  *               one each
- * n_q a multiple of n_kv, up to LN_KV4_MAX_HEADS. 0 <= T < 2^24, T n_q < 2^31, 1 <= B < 2^20,
+ * n_q a multiple of n_kv, up to LN_KV4_MAX_HEADS. 0 <= T < 2^24, T n_q <= 2^30, 1 <= B < 2^20,
  * max_pages >= 1, max_pages page_size <= 2^30, and row blocks of 16 times tiles of 32 keys,
  * (T n_q / n_kv / 16 + B) (max_pages page_size / 32 + 2), fewer than 2^36.
  */

@@ -51,7 +51,7 @@ int check_attention(int64_t T, int64_t B, int32_t n_q, int32_t n_kv, int32_t hea
   const int st = check_dims(page_size, n_kv, head_dim);
   if (st != LN_OK) return st;
   if (n_q > LN_KV4_MAX_HEADS || n_q % n_kv != 0) return LN_ESHAPE;
-  if (T >= kMaxTokens || T * n_q > kMaxDim || B >= int64_t(1) << 20) return LN_ESHAPE;
+  if (T >= kMaxTokens || T * n_q > int64_t(1) << 30 || B >= int64_t(1) << 20) return LN_ESHAPE;
   if (max_pages > (int64_t(1) << 30) / page_size) return LN_ESHAPE;
   if ((T * (n_q / n_kv) / 16 + B) * (max_pages * page_size / 32 + 2) >= int64_t(1) << 36) return LN_ESHAPE;
   return LN_OK;

@@ -35,6 +35,7 @@ constexpr int kWaves = 4;
 constexpr int kTile = 32;             // keys of a wave's tile
 constexpr float kLowest = -3.0e38f;   // the maximum of no keys
 constexpr float kBar = 8.f;           // p stays below 2^8
+constexpr uint32_t kNoNumber = 0x7FC07FC0u;  // a step and a least value
 constexpr int kListed = 512;         // sequences whose steps are summed in LDS
 
 // 16-row tiles of a row block at most, and the waves a SIMD that the registers are cut for
@@ -341,22 +342,38 @@ struct Wave {
       for (int i = 0; i < NP; ++i) r.p[i] = from[(2 * i + lane / kTile) * page_size];
     }
   }
-  // Scales of values that no row sees may be no numbers: keys outside [lo, hi) get zeros.
-  __device__ __forceinline__ void put_key_scales(const Raw& r, int key0, int lo, int hi, float scale2) {
+  // The keys of a tile, a bit each, whose values have a step or least value that is infinite or no
+  // number. Where some row does not see them they must not reach its sums, in which their weight is 0:
+  // their scales become 0, and the least values of their keys no numbers, so that the rows that see
+  // them have no numbers (the others' scores are replaced).
+  static __device__ __forceinline__ uint32_t improper(const Raw& keys, const Raw& values) {
+    uint64_t bad = 0;
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      const uint32_t w = NG == 1 ? keys.p[i] : values.p[i];
+      bad |= __ballot((w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u);
+    }
+    return static_cast<uint32_t>(bad >> 32) | (NG == 1 ? 0u : static_cast<uint32_t>(bad));
+  }
+  // Keys outside [lo, hi), which no row sees, may have any scales too: those of their values become 0.
+  __device__ __forceinline__ void put_key_scales(const Raw& r, int key0, int lo, int hi, float scale2, uint32_t bad) {
+    const int lane = threadIdx.x & 63, key = key0 + lane % kTile;
+    const bool is_bad = (bad >> (lane % kTile)) & 1;
     if constexpr (NG == 1) {
-      const int lane = threadIdx.x & 63, key = key0 + lane % kTile;
       const bool value = lane >= kTile;
-      put(lane, value && (key < lo || key >= hi) ? 0u : r.p[0], value ? 1.f : scale2, value ? 8.f : 0.f);
+      put(lane, value && (key < lo || key >= hi || is_bad) ? 0u : is_bad ? kNoNumber : r.p[0], value ? 1.f : scale2,
+          value ? 8.f : 0.f);
     } else {
 #pragma unroll
-      for (int i = 0; i < NP; ++i) put(64 * i + (threadIdx.x & 63), r.p[i], scale2, 0.f);
+      for (int i = 0; i < NP; ++i) put(64 * i + lane, is_bad ? kNoNumber : r.p[i], scale2, 0.f);
     }
   }
-  __device__ __forceinline__ void put_value_scales(const Raw& r, int key0, int lo, int hi) {
+  __device__ __forceinline__ void put_value_scales(const Raw& r, int key0, int lo, int hi, uint32_t bad) {
     if constexpr (NG > 1) {
       const int lane = threadIdx.x & 63, key = key0 + lane % kTile;
+      const bool zero = key < lo || key >= hi || ((bad >> (lane % kTile)) & 1);
 #pragma unroll
-      for (int i = 0; i < NP; ++i) put(NG * kTile + 64 * i + lane, key < lo || key >= hi ? 0u : r.p[i], 1.f, 8.f);
+      for (int i = 0; i < NP; ++i) put(NG * kTile + 64 * i + lane, zero ? 0u : r.p[i], 1.f, 8.f);
     }
   }
   __device__ __forceinline__ void put(int at, uint32_t word, float times, float code) {
@@ -422,7 +439,6 @@ struct Wave {
         if (key < max(first[t], lo) || key >= last[t]) x[t][e >> 2][e & 3] = -__builtin_inff();
       }
   }
-
   // The tile's part of the sums.
   template <int NT>
   __device__ __forceinline__ void sum(const Raw& r) {
@@ -435,11 +451,12 @@ struct Wave {
       if (__any(top > bar[t])) {
         top = fmaxf(top, __shfl_xor(top, 16));
         top = fmaxf(top, __shfl_xor(top, 32));
-        // what is subtracted rises by the tile's largest score where that is positive; of a
-        // query's first keys (its sums are 0) it goes to their largest, which may lie far below 0
+        // what is subtracted rises by the tile's largest score where that passes the bar (a query's
+        // sums do not depend on its neighbours); of a query's first keys (its sums are 0) it goes
+        // to their largest, which may lie far below 0
         const bool new_query = bar[t] != kBar;
         const float was = m[t];
-        m[t] += new_query ? (top < kLowest ? 0.f : top) : fmaxf(top, 0.f);
+        m[t] += new_query ? (top < kLowest ? 0.f : top) : top > kBar ? top : 0.f;
         bar[t] = new_query && top < kLowest ? kLowest : kBar;
         const float rise = m[t] - was, f = new_query ? 1.f : __builtin_amdgcn_exp2f(-rise);
 #pragma unroll
@@ -542,15 +559,16 @@ struct Wave {
       // A tile's second half goes first where waves meet: the first one (the older wave's, at equal
       // priority) leaves the younger wave behind, to end alone (a chunk of 512 tokens 263 -> 251 us)
       __builtin_amdgcn_s_setprio(0);
-      put_key_scales(keys, key0, lo, k.hi, g.scale2);
+      const uint32_t bad = border ? improper(keys, values) : 0;
+      put_key_scales(keys, key0, lo, k.hi, g.scale2, bad);
       score<NT>(keys);
       if (more) place(t, next_slot, page);  // (the last tile is loaded again: counted waits need no two ways)
       load_keys(g, row, par, keys);
       next_slot = slot_of(min(t + STEP, t_end - 1));
       page = table[next_slot];
-      if (border) hide<NT>(key0, lo);
       __builtin_amdgcn_s_setprio(1);
-      put_value_scales(values, key0, lo, k.hi);
+      put_value_scales(values, key0, lo, k.hi, bad);
+      if (border) hide<NT>(key0, lo);
       sum<NT>(values);
       load_values(g, row, par, values);
     } while (more);
@@ -603,11 +621,11 @@ struct Out {
     if (whole) {
       const int j = (k.row0 + row) / g.heads;
       const int64_t out = static_cast<int64_t>(k.c0 + j) * g.a.n_q + h * g.heads + k.row0 + row - j * g.heads;
-      const float inv = l > 0.f ? 1.f / l : 0.f;
+      const float inv = l == 0.f ? 0.f : 1.f / l;
       *reinterpret_cast<uint2*>(g.a.y + out * D + d) =
           uint2{pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv)};
       if (g.a.lse != nullptr && d == 0)
-        g.a.lse[out] = l > 0.f ? (m + __builtin_log2f(l)) * 0.69314718055994531f : -__builtin_inff();
+        g.a.lse[out] = l == 0.f ? -__builtin_inff() : (m + __builtin_log2f(l)) * 0.69314718055994531f;
     } else {
       *reinterpret_cast<float4*>(g.part_o + (slot * g.rows + row) * D + d) = o;
       if (d == 0) *reinterpret_cast<float2*>(g.part_ml + (slot * g.rows + row) * 2) = float2{m, l};

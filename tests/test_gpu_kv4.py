@@ -288,6 +288,31 @@ def test_scale_and_large_scores(q):
         b.check(y, lse, scale=scale)
 
 
+def test_no_numbers_stay_where_they_are(q):
+    """A query of NaN or infinities gives no numbers in its own rows only; a key or value of such,
+    in those of the queries that see it only."""
+    seqs = [(20, 90), (1, 40), (5, 5)]
+    b = Batch(31, seqs, 4, 2, 64, 32, 32)
+    cu = torch.from_numpy(b.cu).cuda()
+    want = q.kv4_attention(*b.args, cu_q=cu)
+    x = b.args[0].clone()
+    x[3, 1], x[22, 2] = float("nan"), float("inf")
+    y = q.kv4_attention(x, *b.args[1:], cu_q=cu)
+    same = torch.ones(26, 4, dtype=torch.bool)
+    same[3, 1] = same[22, 2] = False
+    assert torch.equal(y[same], want[same]) and not torch.isfinite(y[~same].float()).any()
+    for which, bad in ((1, float("nan")), (3, float("nan")), (1, float("inf")), (3, float("-inf"))):
+        for head in range(2):
+            cache = [t.clone() for t in b.cache]
+            at = 83  # sequence 0's queries from its 13th on see this key
+            cache[which][int(b.table[0, at // 32]), head, :, at % 32] = bad
+            y = q.kv4_attention(b.args[0], cache, *b.args[2:], cu_q=cu)
+            clean = torch.ones(26, 4, dtype=torch.bool)
+            clean[13:20, 2 * head:2 * head + 2] = False
+            assert torch.equal(y[clean], want[clean]), (which, bad, head)
+            assert which == 1 or not torch.isfinite(y[~clean].float()).any()
+
+
 def test_rows_left_alone_and_strides(q):
     """Queries as part of a wider matrix; rows of no sequence, before and behind, are not written."""
     b = Batch(11, [(3, 200), (1, 90)], 8, 2, 64, 32, 32)
