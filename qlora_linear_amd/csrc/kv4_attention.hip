@@ -1,8 +1,8 @@
 // Attention over the paged 4-bit cache (gfx950). Layout and definitions: kv4.h.
 //
 //     y = sum_t p_t v_t / sum_t p_t,   p_t = 2^(c q.k_t - m),   c = scale log2 e
-// in one pass over the keys with a running maximum m. The matrix instruction multiplies codes,
-// which widen to bf16 exactly; steps and least values are applied to its 16 x 16 results:
+// in one pass over the keys with a running m. The matrix instruction multiplies codes, which widen
+// to bf16 exactly; steps and least values are applied to its 16 x 16 results:
 //     q.k_t  = sum_g s_tg (q_g . c_tg) + lo_tg sum(q_g)
 //     y_g    = sum_t (p_t s_tg) (c_tg - 8) + sum_t p_t (lo_tg + 8 s_tg)
 // (around 8 the rounding of p s to bf16 multiplies the deviation from the middle of the range,
@@ -12,15 +12,23 @@
 // its columns (16 a tile: the tokens of a sequence times the query heads of a key head), so that
 // a lane's results are eight keys of one query. That is the operand of the second product as it
 // is, whose rows are elements of the head: nothing moves between lanes in a tile, and codes
-// reach the lanes that multiply them straight from global memory, 16 rows of a key tile at a
-// time. The maximum is raised only when a score passes it by 2^8 (a vote); p then stays below
-// 2^8, which costs no accuracy, and the cross-lane maximum and the rescaling drop out of most tiles.
+// reach the lanes that multiply them straight from global memory. m is raised only when a score
+// passes it by 2^8 (a vote); p then stays below 2^8, which costs no accuracy, and the cross-lane
+// maximum and the rescaling drop out of most tiles.
 //
-// The four waves of a workgroup take every fourth tile of a row block (up to 16 NQ rows of one
-// sequence and key head) and join in LDS. Row blocks and their key tiles, in steps of four, are
-// laid end to end, and each workgroup takes an equal share of that line, whatever the sequences'
-// lengths: a row block that is cut is written as float32 parts, which a second launch joins in
-// order.
+// Row blocks, up to 16 NQ rows of one sequence and key head, are laid end to end in units of the
+// time they take, and each worker has an equal share of that line, whatever the sequences'
+// lengths. A worker is a workgroup, whose four waves take every fourth tile and join in LDS, or,
+// where row blocks are many and short, a wave. A row block that is cut is written as float32
+// parts, which a second launch joins in order.
+//
+// What bounds it: with few rows the loads of this pattern and the vector units, by turns (64
+// sequences of up to 16384 keys, 554 MB: 114 us; when the kernel took 150, its loads alone took 113
+// and its arithmetic alone 110). Many rows are bound by the vector units, which overlap little with the
+// matrix units at two waves a SIMD (512 tokens against up to 16384 keys: 250 us, 549 TFLOP/s).
+// Measured and not kept, each against the build of its time: codes as 16 + c by shifts and masks, in
+// place of the conversion (64 sequences 128 -> 159 us); row blocks of 16 rows only (the chunk of
+// 512 tokens 1496 us, 261 with larger ones); twice the workers (1 x 131071 keys 46 -> 59 us).
 #include <algorithm>
 #include <type_traits>
 
@@ -36,7 +44,7 @@ constexpr int kTile = 32;             // keys of a wave's tile
 constexpr float kLowest = -3.0e38f;   // the maximum of no keys
 constexpr float kBar = 8.f;           // p stays below 2^8
 constexpr uint32_t kNoNumber = 0x7FC07FC0u;  // a step and a least value
-constexpr int kListed = 512;         // sequences whose steps are summed in LDS
+constexpr int kListed = 512;          // row blocks whose units are summed in LDS
 
 // 16-row tiles of a row block at most, and the waves a SIMD that the registers are cut for
 // (workgroups a CU, then): as many as need no scratch memory.
@@ -59,7 +67,7 @@ __device__ __forceinline__ int64_t uniform(int64_t v) {
 typedef const __attribute__((address_space(4))) int32_t* Const;
 
 struct Plan {
-  bool solo;         // the workers that share the steps are waves, not workgroups
+  bool solo;         // workers are waves, not workgroups
   int workers;
   int items;         // row blocks at most
   int in_seq;        // row blocks of a sequence, where workgroups sum the units themselves; else 0
@@ -849,10 +857,13 @@ __global__ __launch_bounds__(kThreads) void kv4_join_kernel(Args g) {
   }
 }
 
-// Workers of their own are waves where there are row blocks enough that each has few parts.
+// Workers are waves where there are row blocks enough that each has few parts. Workgroups -> waves:
+// prompts of 2500 tokens 188 -> 135 us, 96 x 40 heads 122 -> 110; below the limit 1 x 131071 keys 41 ->
+// 92, 64 sequences of 8 heads 114 -> 121 (5 tokens of 16 sequences, though, 59 -> 54).
 bool solo_of(int64_t items, int n_kv) { return items * n_kv >= 1024; }
 
-// Rows of a row block: 16, 32 or 64, as many as a sequence's new tokens fill.
+// Rows of a row block: 16, 32 or 64, as many as a sequence's new tokens fill; without a bound the
+// average's.
 Plan plan_of(int64_t T, int64_t B, int n_q, int n_kv, int head_dim, int max_q, int64_t max_len, int group) {
   const int64_t heads = n_q / n_kv;
   const int64_t most = max_q > 0 ? max_q * heads : (T * heads + B - 1) / B;
@@ -868,7 +879,7 @@ Plan plan_of(int64_t T, int64_t B, int n_q, int n_kv, int head_dim, int max_q, i
   if (p.by_head && static_cast<int64_t>(p.items) * n_kv >= p.workers) p.by_head = false;
   p.cuts = p.by_head ? p.items * n_kv : p.workers;
   // Up to 512 keys are four tiles a wave, which take no longer than a second launch does (a token
-  // after 500 keys in a call XX us, YY in two launches).
+  // after 500 keys, back-to-back calls: 12.0 us, 15.2 in two launches).
   p.whole = p.in_seq != 0 && !p.solo && max_len <= 512 && static_cast<int64_t>(p.items) * n_kv <= p.workers;
   if (p.whole) p.workers = p.items * n_kv, p.by_head = false, p.cuts = 0;
   return p;
