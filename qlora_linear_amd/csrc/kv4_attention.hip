@@ -47,7 +47,8 @@ constexpr uint32_t kNoNumber = 0x7FC07FC0u;  // a step and a least value
 constexpr int kListed = 512;          // row blocks whose units are summed in LDS
 
 // 16-row tiles of a row block at most, and the waves a SIMD that the registers are cut for
-// (workgroups a CU, then): as many as need no scratch memory.
+// (workgroups a CU, then): as many as need no scratch memory, but for four registers of <64, 64, 4>
+// with workgroups as workers. 48 rows of heads of 128 spill 24 to 156.
 constexpr int most_nq(int D, int G) { return D == 64 ? (G == 64 ? 4 : 2) : D == 128 ? 2 : 1; }
 constexpr int waves_of(int D, int G, int NQ, bool SOLO) {
   if (D == 64) return NQ == 1 ? 4 : NQ == 2 && (SOLO || G == 64) ? 3 : 2;
@@ -859,7 +860,8 @@ __global__ __launch_bounds__(kThreads) void kv4_join_kernel(Args g) {
 
 // Workers are waves where there are row blocks enough that each has few parts. Workgroups -> waves:
 // prompts of 2500 tokens 188 -> 135 us, 96 x 40 heads 122 -> 110; below the limit 1 x 131071 keys 41 ->
-// 92, 64 sequences of 8 heads 114 -> 121 (5 tokens of 16 sequences, though, 59 -> 54).
+// 92, 64 sequences of 8 heads 114 -> 121. Several tokens below it go either way (8 of 16 sequences of 32
+// query heads 45 -> 39, 4 of 64 sequences 39 -> 47).
 bool solo_of(int64_t items, int n_kv) { return items * n_kv >= 1024; }
 
 // Rows of a row block: 16, 32 or 64, as many as a sequence's new tokens fill; without a bound the
