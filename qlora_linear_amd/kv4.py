@@ -40,6 +40,7 @@ KV4_SYMBOLS = tuple(_KV4_SIGS)
 
 _PLAIN = {torch.float32: LN_F32, torch.bfloat16: LN_BF16}
 _GROUPS, _DIMS = (32, 64, 128), (64, 128, 256)
+_MOST = 2 ** 31 - 1  # ctypes takes larger ones modulo 2^32
 
 
 def kv4_cache(n_pages: int, n_kv: int, head_dim: int, page_size: int = 32, group: int = 64, device="cuda"):
@@ -209,6 +210,8 @@ def kv4_attention(q, cache, block_table, lens, *, cu_q=None, max_q: int | None =
         bound = 0 if max_q is None else max_q
         if max_q is not None and max_q < 1:
             raise ValueError(f"max_q must be at least 1, got {max_q}")
+    if window > _MOST or bound > _MOST or window < -_MOST:
+        raise ValueError(f"window and max_q must be below 2^31, got {window} and {max_q}")
     if out is None:
         out = q.new_empty(q.shape)
         yp = out.data_ptr()

@@ -548,3 +548,14 @@ def test_refusals_on_gpu(q):
     assert q.kv4_append(empty, empty, empty, c, s[:0]).shape == (0, 2, 64)
     assert q.kv4_read(c, s[:0])[0].shape == (0, 2, 64)
     assert q.kv4_attention(empty, c, t, n, cu_q=torch.zeros(5, dtype=torch.int32).cuda()).shape == (0, 2, 64)
+
+
+def test_large_windows_are_refused(q):
+    c = q.kv4_cache(3, 2, 64)
+    x = torch.zeros(4, 2, 64, dtype=BF).cuda()
+    t, n, cu = torch.zeros(4, 3, dtype=torch.int32).cuda(), torch.ones(4, dtype=torch.int32).cuda(), torch.arange(5, dtype=torch.int32).cuda()
+    for kw in (dict(window=2 ** 31), dict(window=2 ** 32), dict(window=2 ** 32 + 5), dict(window=-2 ** 32 + 5),
+               dict(cu_q=cu, max_q=2 ** 32 + 1)):
+        with pytest.raises(ValueError, match="2\\^31"):
+            q.kv4_attention(x, c, t, n, **kw)
+    q.kv4_attention(x, c, t, n, window=2 ** 31 - 1)
