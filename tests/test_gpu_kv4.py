@@ -559,3 +559,24 @@ def test_large_windows_are_refused(q):
         with pytest.raises(ValueError, match="2\\^31"):
             q.kv4_attention(x, c, t, n, **kw)
     q.kv4_attention(x, c, t, n, window=2 ** 31 - 1)
+
+
+@pytest.mark.parametrize("dtype", [BF, F])
+def test_append_many_tokens_of_few_slots(q, dtype):
+    """Tokens that go in several launches: the last of a slot, wherever it is, and every query."""
+    T, D, n_q, n_kv, n = 70001, 64, 3, 2, 2000
+    g = torch.Generator(device="cuda").manual_seed(5)
+    x, k, v = (torch.randn(T, h, D, generator=g, device="cuda").to(dtype) for h in (n_q, n_kv, n_kv))
+    slots = torch.randint(-1, n, (T,), generator=g, device="cuda")
+    slots[-1] = slots[7]
+    pos = torch.randint(0, 11, (T,), generator=g, device="cuda")  # (9 and 10 are in no table)
+    cos, sin = (torch.from_numpy(t).cuda() for t in tables(9, D))
+    a, b = (q.kv4_cache(n // 32 + 1, n_kv, D) for _ in range(2))
+    y = q.kv4_append(x, k, v, a, slots, cos=cos, sin=sin, positions=pos)
+    last = {s: t for t, (s, p) in enumerate(zip(slots.tolist(), pos.tolist())) if s >= 0 and p < 9}
+    keep = torch.tensor(sorted(last.values())).cuda()
+    q.kv4_append(None, k[keep], v[keep], b, slots[keep], cos=cos, sin=sin, positions=pos[keep])
+    assert all(torch.equal(s, t) for s, t in zip(a, b))
+    for i in range(0, T, 500):  # (calls of one launch)
+        e = slice(i, min(i + 500, T))
+        assert torch.equal(y[e], q.kv4_append(x[e], k[e], v[e], b, slots[e], cos=cos, sin=sin, positions=pos[e]))
