@@ -71,7 +71,7 @@ __device__ __forceinline__ uint32_t codes8(const float (&x)[8], float lo, float 
 // x c + y s of eight elements as bf16, as float64 sums that are rounded to float32 and then to
 // bf16 (a product of two float32 is exact there). The float32 sum is off by less than e, its
 // two roundings and the product's; where bf16 has the same neighbour for both ends, that is the one,
-// else (a wave in eight) the eight are summed in float64.
+// else (in a wave in five) the eight are summed in float64.
 __device__ __forceinline__ uint4 rotated8(const float (&x)[8], const float (&y)[8], const float (&c)[8],
                                           const float (&s)[8]) {
   uint32_t lo[4], hi[4], unlike = 0;
