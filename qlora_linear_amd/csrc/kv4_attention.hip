@@ -261,6 +261,14 @@ struct Scales {
   float step[2][NG][kTile], base[2][NG][kTile];  // [keys, values]
 };
 
+// What the lanes of a wave wrote to LDS above is there for all of them below, and what they read above
+// is not written before. (The LDS serves a wave's accesses in their order, so this is the compiler's
+// order alone, and no instruction.)
+__device__ __forceinline__ void wave_in_order() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
+  __builtin_amdgcn_wave_barrier();
+}
+
 template <int D, int G, int NQ>
 struct Wave {
   static constexpr int C = D / 32, NG = D / G, CG = G / 32;
@@ -569,7 +577,9 @@ struct Wave {
       // priority) leaves the younger wave behind, to end alone (a chunk of 512 tokens 263 -> 251 us)
       __builtin_amdgcn_s_setprio(0);
       const uint32_t bad = border ? improper(keys, values) : 0;
+      wave_in_order();
       put_key_scales(keys, key0, lo, k.hi, g.scale2, bad);
+      wave_in_order();
       score<NT>(keys);
       if (more) place(t, next_slot, page);  // (the last tile is loaded again: counted waits need no two ways)
       load_keys(g, row, par, keys);
@@ -577,6 +587,7 @@ struct Wave {
       page = table[next_slot];
       __builtin_amdgcn_s_setprio(1);
       put_value_scales(values, key0, lo, k.hi, bad);
+      wave_in_order();
       if (border) hide<NT>(key0, lo);
       sum<NT>(values);
       load_values(g, row, par, values);
