@@ -16,9 +16,9 @@ class Batch:
     has hold NaN scales; past a sequence's end the table (`width` columns, or two more than the longest
     needs) names pages that do not exist. levels(b, t): what is added, in powers of two of the
     softmax's weight, to the scores of key t of sequence b, through the keys' least values (queries have
-    mean 1 then)."""
+    mean 1 then); centres(b, t): to its values."""
 
-    def __init__(self, seed, seqs, n_q, n_kv, D, group, page, width=None, step=(0.2, 0.4), levels=None, scale=None):
+    def __init__(self, seed, seqs, n_q, n_kv, D, group, page, width=None, step=(0.2, 0.4), levels=None, centres=None, scale=None):
         g = np.random.default_rng(seed)
         self.seqs, self.n_q, self.n_kv, self.D, self.group, self.page = seqs, n_q, n_kv, D, group, page
         self.scale = D ** -0.5 if scale is None else scale
@@ -36,6 +36,8 @@ class Batch:
                 lo = s * (0.5 * g.standard_normal(s.shape) - 7.5)
                 if levels is not None:
                     lo[0] += levels(b, i * page + np.arange(n)) * np.log(2) / (self.scale * D)
+                if centres is not None:
+                    lo[1] += centres(b, i * page + np.arange(n))
                 scales[:, self.table[b, i], :, :, :n] = np.stack([s, to_bf16(lo.astype(np.float32))], -1)
         codes = lambda *s: np.frombuffer(g.bytes(int(np.prod(s)) * pages * n_kv), np.uint8).reshape(pages, n_kv, *s)  # noqa: E731
         self.np = codes(page, D // 2), scales[0], codes(page // 4, 2 * D), scales[1]

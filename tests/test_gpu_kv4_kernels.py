@@ -30,3 +30,16 @@ def test_waves_as_workers(q, i):
     print("largest share of the bound", batch.check(y, lse, window), flush=True)
     again, _ = attend(q, batch, max_q, window)
     assert torch.equal(again, y)  # the result does not depend on the run
+
+
+@pytest.mark.parametrize("i", range(len(cases.LONG)), ids=lambda i: f"{len(cases.LONG[i][0])}x{cases.LONG[i][0][0][1]}-" +
+                         "-".join(str(x) for x in cases.LONG[i][1:8]))
+def test_long_loops(q, i):
+    """Many tiles and pages a wave; scores that rise and fall on the way."""
+    batch, max_q, window, checked = cases.long_batch(i)
+    print("long", i, cases.LONG[i][1:], flush=True)
+    y, lse = attend(q, batch, max_q, window)
+    for b, h in checked:
+        print("share of the bound", b, h, batch.check(y, lse, window, [b], slice(h, h + 1)), flush=True)
+    again, _ = attend(q, batch, max_q, window)
+    assert torch.equal(again, y)

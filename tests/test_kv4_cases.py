@@ -86,3 +86,85 @@ def test_reference_without_some_keys():
     want, wl = o.attention(b.q.astype(np.float64), k, v, b.scale)
     np.testing.assert_allclose(y[0], want[0], rtol=1e-11, atol=1e-12)
     np.testing.assert_allclose(lse[0], wl[0], rtol=1e-12)
+
+
+# ---- many tiles a wave ---------------------------------------------------------------------
+# A wave's loop over tiles and pages at length, with scores that rise and fall by it. Key levels (powers of two of
+# the weight) by sequence: spikes of 10, one in about 256 keys, over level keys, so that both weigh in the
+# result; slow rises with a fall after each; slow falls with a rise. Values differ by level and place.
+def spikes(b, t):
+    return np.random.default_rng(1000 + b).integers(0, 257, 1 << 17)[t] == 0
+
+
+def levels(b, t):
+    if b % 3 == 0:
+        return np.where(spikes(b, t), 10.0, 0.0)
+    return (t if b % 3 == 1 else -t) % 2000 / 25.0
+
+
+def centres(b, t):
+    return np.where(spikes(b, t), -2.0, 2.0) if b % 3 == 0 else 2 * np.sin(t / 50)
+
+
+LONG = [
+    # sequences, query heads a key head, n_kv, D, group, page, window, max_q, waves as workers, what is checked of them
+    ([(8, 20000 - 37 * b) for b in range(8)], 4, 4, 64, 32, 64, 0, 8, False, [(0, 1), (4, 3), (5, 0)]),
+    ([(1, 26000 - 111 * b) for b in range(4)], 2, 8, 128, 64, 96, 0, 1, False, [(0, 2), (1, 7), (2, 0), (3, 5)]),
+    ([(1, 9000 - 64 * b) for b in range(12)], 8, 8, 256, 128, 32, 7001, 1, False, [(0, 2), (1, 7), (2, 0), (3, 5)]),
+    ([(200, 9000)] + [(1, 7000 - 100 * b) for b in range(8)], 4, 8, 128, 128, 256, 0, 0, False, [(0, 2), (1, 7), (2, 0), (3, 5), (0, 4)]),
+    ([(1, 1900 + b) for b in range(64)], 3, 16, 64, 64, 32, 0, 1, True, [(0, 15), (1, 2), (2, 3), (63, 0), (33, 9)]),
+    ([(5, 1500 - b) for b in range(66)], 5, 16, 64, 32, 64, 1333, 5, True, [(0, 15), (1, 2), (2, 3), (65, 0), (33, 9)]),
+    ([(1, 700 + 5 * b) for b in range(65)], 1, 16, 256, 32, 128, 0, 1, True, [(0, 15), (1, 2), (2, 3), (63, 0), (33, 9)]),
+]
+
+
+def long_batch(i):
+    seqs, heads, n_kv, D, G, page, window, max_q, solo, checked = LONG[i]
+    batch = u.Batch(50 + i, seqs, heads * n_kv, n_kv, D, G, page, step=(0.04, 0.06), levels=levels, centres=centres)
+    return batch, max_q, window, checked
+
+
+def scores(batch, b, h, row, window):
+    """Scores of a row of sequence b and key head h in powers of two, -inf where it does not see a key."""
+    n, L = batch.seqs[b]
+    (kc, ks, kl), _ = batch.parts(b, slice(h, h + 1))
+    x = batch.scale / np.log(2) * (o.values(kc, ks, kl, batch.group)[:, 0] @ batch.rows(b, slice(h, h + 1))[0, row])
+    last = L - n + row // (batch.n_q // batch.n_kv)
+    t = np.arange(L)
+    return np.where((t <= last) & (t > last - window if window else True), x, -np.inf)
+
+
+@pytest.mark.parametrize("i", range(len(LONG)))
+def test_long_loops_are_long(i):
+    """At least eight tiles to nearly every wave, and maxima that are raised after its first tile."""
+    batch, max_q, window, checked = long_batch(i)
+    assert batch.plan(max_q)["solo"] == LONG[i][8]
+    waves = list(batch.waves(max_q, window))
+    steps = np.zeros((max(w[0] for w in waves) + 1, 4), int)
+    for me, _, tiles in waves:
+        steps[me, tiles[0] % 4 if not LONG[i][8] else 0] += len(tiles)
+    per_wave = steps.reshape(-1) if not LONG[i][8] else steps[:, 0]
+    assert np.median(per_wave) >= 8 and max(len(t) for *_, t in waves) >= 8
+    raised = {}
+    for b, h in checked:
+        row0 = 0
+        x = scores(batch, b, h, row0, window)
+        raised[b, h] = sum(u.raises(x, tiles) for _, piece, tiles in waves if piece[:2] == (b, row0) and piece[3] == h)
+    assert sum(raised.values()) >= 5 and any(raised[k] > 0 for k in raised if k[0] % 3 == 0)
+
+
+def test_a_wrong_rescaling_is_found():
+    """Sums that a raise leaves as they were, drops, or scales by the wrong power are off by more than the bound of
+    the reference, on spikes and on a slow rise."""
+    seqs = [(1, 12000)] * 2
+    batch = u.Batch(9, seqs, 1, 1, 64, 64, 64, step=(0.04, 0.06), levels=levels, centres=centres)
+    for b in range(2):
+        x = scores(batch, b, 0, 0, 0)
+        (_, (vc, vs, vl)) = batch.parts(b)
+        v = o.values(vc, vs, vl, 64)[:, 0]
+        waves = [range(s + w, min(s + 40, -(-len(x) // 32)), 4) for s in range(0, -(-len(x) // 32), 40) for w in range(4)]
+        assert sum(u.raises(x, t) for t in waves) >= 10
+        y, _, ey, _ = batch.reference(b)
+        np.testing.assert_allclose(u.summed(x, v, waves), y[0, 0], rtol=1e-9, atol=1e-9)
+        for wrong in (lambda rise: 1.0, lambda rise: 0.0, lambda rise: 2.0 ** rise, lambda rise: 2.0 ** (1 - rise)):
+            assert np.any(np.abs(u.summed(x, v, waves, wrong) - y[0, 0]) > ey[0, 0]), b
