@@ -1,8 +1,10 @@
 """Every kernel of the paged 4-bit cache, against a float64 reference within a bound counted from
 its roundings, in batches that are shown on the host to reach it."""
+import numpy as np
 import pytest
 import torch
 
+from oracle import kv4 as o
 from tests import test_kv4_cases as cases
 
 pytestmark = pytest.mark.gpu
@@ -43,3 +45,70 @@ def test_long_loops(q, i):
         print("share of the bound", b, h, batch.check(y, lse, window, [b], slice(h, h + 1)), flush=True)
     again, _ = attend(q, batch, max_q, window)
     assert torch.equal(again, y)
+
+
+# ---- append: prompts -----------------------------------------------------------------------
+# Tokens whose slots run on in scattered pages, as a prompt's do: values of four tokens at once.
+# T, n_q, n_kv, D, group, page, rot, interleaved, dtype, first slot of the run
+RUNS = [
+    (600, 4, 3, 64, 32, 32, 64, False, torch.bfloat16, 0), (777, 2, 9, 64, 64, 96, 0, False, torch.float32, 4),
+    (515, 3, 5, 128, 64, 64, 128, True, torch.bfloat16, 0), (1025, 4, 4, 128, 128, 32, 64, False, torch.float32, 28),
+    (513, 2, 5, 256, 128, 32, 256, False, torch.bfloat16, 8), (801, 6, 2, 256, 32, 64, 16, True, torch.float32, 0),
+    (640, 2, 2, 128, 32, 64, 128, False, torch.bfloat16, 1), (700, 1, 1, 64, 64, 32, 32, True, torch.bfloat16, 2),
+    (999, 1, 2, 256, 64, 128, 0, False, torch.bfloat16, 31), (9001, 2, 2, 64, 32, 256, 64, False, torch.bfloat16, 8),
+    (8192 + 514, 1, 1, 128, 64, 32, 0, False, torch.float32, 12),
+]
+
+
+@pytest.mark.parametrize("case", RUNS, ids=lambda c: "-".join(str(x).removeprefix("torch.") for x in c))
+@pytest.mark.parametrize("broken", [False, True])
+def test_append_runs(q, case, broken):
+    """Stored codes and scales, bit for bit. broken: within fours of tokens some have no slot, the slot of
+    another (of which the last is kept) or no position."""
+    T, n_q, n_kv, D, group, page, rot, inter, dtype, first = case
+    print("runs", case, broken, flush=True)
+    g = np.random.default_rng(T + D + first)
+    pages = (first + T - 1) // page + 4
+    at = first + np.arange(T)
+    slots = g.permutation(pages)[at // page] * page + at % page
+    n_pos = T + 40
+    pos = 37 + np.arange(T)
+    if broken:
+        for t in range(5, T, 37):  # (every place within four and within a tile)
+            kind = t // 37 % 4
+            if kind == 0:
+                slots[t] = -1
+            elif kind == 1:
+                slots[t] = slots[t - 1 - t % 5]
+            elif kind == 2:
+                slots[t] = slots[min(t + 1, T - 1)]
+            else:
+                pos[t] = n_pos
+    fours = sum(slots[t] % 4 == 0 and np.array_equal(slots[t:t + 4], slots[t] + np.arange(4)) for t in range(0, T - 3, 4))
+    assert fours > T / 8 if first % 4 == 0 else fours == 0
+    cache = q.kv4_cache(pages, n_kv, D, page, group)
+    for t in cache:
+        t.view(torch.uint8).random_(0, 250)
+    before = tuple(t.float().cpu().numpy() if t.dtype is torch.bfloat16 else t.cpu().numpy() for t in cache)
+    rows = [torch.from_numpy(g.standard_normal((T, n, D)).astype(np.float32)).to(dtype) for n in (n_q, n_kv, n_kv)]
+    turned = [a.double().numpy() for a in rows]
+    kw, placed = {}, np.ones(T, bool)
+    if rot:
+        angle = np.arange(n_pos)[:, None] * 1e4 ** (-np.arange(0, rot, 2) / rot)
+        cos, sin = np.cos(angle).astype(np.float32), np.sin(angle).astype(np.float32)
+        kw = dict(cos=torch.from_numpy(cos).cuda(), sin=torch.from_numpy(sin).cuda(), positions=torch.from_numpy(pos).cuda(),
+                  interleaved=inter)
+        placed = pos < n_pos
+        turned[:2] = [o.rotate(a, cos, sin, np.where(placed, pos, 0), inter) for a in turned[:2]]
+    got = q.kv4_append(*(a.cuda() for a in rows), cache, torch.from_numpy(slots).cuda(), **kw)
+    assert np.array_equal(got.float().cpu().numpy(), o.rounded(turned[0]) * placed[:, None, None])
+    after = tuple(t.float().cpu().numpy() if t.dtype is torch.bfloat16 else t.cpu().numpy() for t in cache)
+    last = {int(slots[t]): t for t in range(T) if placed[t] and slots[t] >= 0}
+    keep, where = np.array(list(last.values())), np.array(list(last))
+    for have, want in zip(o.read(after, where), (o.quantize(o.rounded(a[keep]), group) for a in turned[1:])):
+        for a, b in zip(have, want):
+            assert np.array_equal(a, b)
+    others = np.setdiff1d(np.arange(pages * page), where)
+    for have, want in zip(o.read(after, others), o.read(before, others)):
+        for a, b in zip(have, want):
+            assert np.array_equal(a, b, equal_nan=a.dtype.kind == "f")
