@@ -5,6 +5,7 @@ import pytest
 import torch
 
 from oracle import kv4 as o
+from tests import kv4_util as u
 from tests import test_kv4_cases as cases
 
 pytestmark = pytest.mark.gpu
@@ -112,3 +113,17 @@ def test_append_runs(q, case, broken):
     for have, want in zip(o.read(after, others), o.read(before, others)):
         for a, b in zip(have, want):
             assert np.array_equal(a, b, equal_nan=a.dtype.kind == "f")
+
+
+# ---- attention: the one launch, values that are no numbers, missing pages ------------------
+@pytest.mark.parametrize("D,G", cases.DIMS)
+@pytest.mark.parametrize("n,heads", [(1, 4), (6, 4), (5, 13)])
+@pytest.mark.parametrize("page,window", [(32, 0), (64, 100), (96, 0)])
+def test_up_to_512_keys_in_one_launch(q, D, G, n, heads, page, window):
+    width = 512 // page
+    seqs = [(n, L) for L in (min(500, width * page), 0, 1, 33, width * page, 256)]
+    batch = u.Batch(D + G + n, seqs, 2 * heads, 2, D, G, page, width=width)
+    assert batch.plan(n)["whole"]
+    print("one launch", D, G, n, heads, page, window, flush=True)
+    y, lse = attend(q, batch, n, window)
+    batch.check(y, lse, window)
