@@ -127,3 +127,27 @@ def test_up_to_512_keys_in_one_launch(q, D, G, n, heads, page, window):
     print("one launch", D, G, n, heads, page, window, flush=True)
     y, lse = attend(q, batch, n, window)
     batch.check(y, lse, window)
+
+
+@pytest.mark.parametrize("D,G,heads", [(64, 32, 2), (128, 128, 2), (256, 64, 3), (64, 64, 4)])
+@pytest.mark.parametrize("key", [83, 20])  # one that some queries see, one in a tile that all see
+def test_no_numbers_reach_every_query_that_sees_them(q, D, G, heads, key):
+    """NaN or an infinity in a value's scales, NaN in a key's: no finite element in the rows of the queries that
+    see it, the others' the same bits. (An infinite key may win or lose all of the weight.)"""
+    batch = u.Batch(31, [(20, 90), (1, 40), (5, 5)], 2 * heads, 2, D, G, 32)
+    x, cache, table, lens = batch.device()
+    kw = dict(cu_q=torch.from_numpy(batch.cu).cuda())
+    want = q.kv4_attention(x, cache, table, lens, **kw)
+    batch.check(want)
+    assert torch.isfinite(want.float()).all()
+    first = max(0, key - 70)  # of sequence 0's queries, the first that sees it
+    for which, bad in ((1, float("nan")), (3, float("nan")), (3, float("inf")), (3, float("-inf"))):
+        for part in (slice(0, 2), slice(0, 1), slice(1, 2)):  # step and least value, one of them
+            for h in range(2):
+                changed = [t.clone() for t in cache]
+                changed[which][int(table[0, key // 32]), h, :, key % 32, part] = bad
+                y = q.kv4_attention(x, changed, table, lens, **kw)
+                clean = torch.ones(26, 2 * heads, dtype=torch.bool)
+                clean[first:20, h * heads:(h + 1) * heads] = False
+                assert torch.equal(y[clean], want[clean]), (which, bad, part, h)
+                assert not torch.isfinite(y[~clean].float()).any(), (which, bad, part, h)
