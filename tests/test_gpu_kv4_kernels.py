@@ -151,3 +151,18 @@ def test_no_numbers_reach_every_query_that_sees_them(q, D, G, heads, key):
                 clean[first:20, h * heads:(h + 1) * heads] = False
                 assert torch.equal(y[clean], want[clean]), (which, bad, part, h)
                 assert not torch.isfinite(y[~clean].float()).any(), (which, bad, part, h)
+
+
+@pytest.mark.parametrize("D,G,page", [(64, 64, 32), (128, 32, 64), (256, 128, 32)])
+@pytest.mark.parametrize("window", [0, 90])
+def test_a_missing_page_has_no_keys(q, D, G, page, window):
+    batch = u.Batch(7, [(3, 5 * page + 9), (1, 2 * page)], 4, 2, D, G, page)
+    x, cache, table, lens = batch.device()
+    cu = torch.from_numpy(batch.cu).cuda()
+    for pages, bad in (((1,), -1), ((0, 3), cache[0].shape[0]), ((5,), 2 ** 31 - 1), ((0, 1, 2, 3, 4), -2 ** 31)):
+        broken = table.clone()
+        broken[0, list(pages)] = bad
+        print("missing", pages, bad, flush=True)
+        y, lse = q.kv4_attention(x, cache, broken, lens, cu_q=cu, window=window, return_lse=True)
+        batch.check(y, lse, window, [0], missing=[t for p in pages for t in range(p * page, min((p + 1) * page, 5 * page + 9))])
+        batch.check(y, lse, window, [1])
