@@ -110,7 +110,8 @@ int kv4_read(int64_t T, const int64_t* slots, const ln_kv4_cache* cache, int out
  * Query head i reads key head i / (n_q / n_kv). A query that sees no key (an empty sequence,
  * more queries than keys) gives y = 0 and lse = -infinity. Products of q (bf16) with codes
  * and all sums are float32; p_t s_t is rounded to bf16 before it multiplies c_t - 8 (off by at
- * most 2^-8 p_t s_t |c_t - 8| a key); y is rounded once.
+ * most 2^-8 p_t s_t |c_t - 8| a key); y is rounded once. p_t stands there for a weight below 2^8 that is
+ * divided by the weights' sum at the end, so scale log2 e q k_t and 2^8 sum_t |v_t| must be finite in float32.
  *   q           bf16 [T] rows of n_q heads, q_stride elements apart (a multiple of 8, at least
  *               a row)
  *   cu_q        int32 [B + 1]: sequence b has rows cu_q[b] .. cu_q[b + 1] - 1 (clamped to
@@ -120,7 +121,7 @@ int kv4_read(int64_t T, const int64_t* slots, const ln_kv4_cache* cache, int out
  *   lens        int32 [B] (clamped to 0 .. max_pages page_size)
  *   block_table int32 [B][max_pages]. A page out of range has no keys
  *   window      0: none
- *   scale       > 0, finite
+ *   scale       > 0, scale log2 e finite in float32
  *   y           bf16 [T][n_q head_dim] contiguous;  lse  float32 [T][n_q] or NULL (outputs).
  *               Rows of no sequence are left as they were
  *   workspace   kv4_attention_workspace_bytes(...) bytes, where a sequence's keys are split

@@ -132,7 +132,7 @@ int kv4_attention(int64_t T, int64_t B, int32_t n_q, const uint16_t* q, int64_t 
                   size_t workspace_bytes, void* stream) {
   int st = check_cache(cache);
   if (st != LN_OK) return st;
-  if (window < 0 || !std::isfinite(scale) || !(scale > 0.f)) return LN_EINVAL;
+  if (window < 0 || !std::isfinite(scale * kLog2E) || !(scale > 0.f)) return LN_EINVAL;
   st = check_attention(T, B, n_q, cache->n_kv, cache->head_dim, max_q, max_pages, cache->page_size);
   if (st != LN_OK) return st;
   if (cu_q == nullptr && T != B) return LN_ESHAPE;

@@ -975,7 +975,7 @@ hipError_t launch_kv4_attention(const Kv4Attention& a, const ln_kv4_cache& c, vo
   g.rows = 16 * p.nq;
   g.tiles_per_page = c.page_size / kTile;
   g.page_inv = static_cast<uint32_t>(((uint64_t(1) << 32) + g.tiles_per_page - 1) / g.tiles_per_page);
-  g.scale2 = a.scale * 1.4426950408889634f;
+  g.scale2 = a.scale * kLog2E;
   g.workers = p.workers;
   g.by_head = p.by_head;
   g.whole = p.whole;

@@ -27,6 +27,8 @@ hipError_t launch_kv4_append(const Kv4Append& a, bool bf16, const ln_kv4_cache& 
 hipError_t launch_kv4_read(int64_t T, const int64_t* slots, const ln_kv4_cache& c, bool bf16, void* k, void* v,
                            hipStream_t stream);
 
+constexpr float kLog2E = 1.4426950408889634f;
+
 struct Kv4Attention {
   int T, B, n_q;
   const uint16_t* q;

@@ -110,10 +110,10 @@ class Batch:
         # sums over keys, of one key after another at the worst and twice a rounding, and of the parts
         adds = (2 * L + 128) * U
         el = (w * rel).sum(-1) + adds + 4 * U * (np.abs(np.where(some, lse, 0)) + most + 16)
-        # y: the weights, l, p s to bf16 against c - 8, the sums of c and of 8 apart, y to bf16; weights
-        # below the least float32
+        # y: the weights, l, p s to bf16 against c - 8, the sums of c and of 8 apart, y to bf16; weights, and
+        # p s against |c - 8| <= 8, below the least normal float32
         ey = (w * rel) @ np.abs(v) + el[..., None] * np.abs(y) + UB * (w @ dev) + 2 * adds * (w @ size) + UB * np.abs(y)
-        ey = ey + 2.0 ** -120 * size.sum(1)[:, None]
+        ey = ey + 2.0 ** -120 * size.sum(1)[:, None] + L * 2.0 ** -122
         return y, lse, np.where(some[:, None], 1.02 * ey, 0), np.where(some, 1.02 * el, 0)
 
     def check(self, y, lse=None, window=0, seqs=None, heads=slice(None), missing=()):

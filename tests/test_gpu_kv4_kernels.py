@@ -166,3 +166,11 @@ def test_a_missing_page_has_no_keys(q, D, G, page, window):
         y, lse = q.kv4_attention(x, cache, broken, lens, cu_q=cu, window=window, return_lse=True)
         batch.check(y, lse, window, [0], missing=[t for p in pages for t in range(p * page, min((p + 1) * page, 5 * page + 9))])
         batch.check(y, lse, window, [1])
+
+
+@pytest.mark.parametrize("far", [2.0 ** 90, 2.0 ** -90])
+def test_far_keys_and_values(q, far):
+    """Keys and values of far magnitudes, whose scores are ordinary by the scale."""
+    batch = u.Batch(3, [(1, 700), (4, 300)], 8, 2, 128, 64, 32, step=(0.2 * far, 0.4 * far), scale=0.1 / far)
+    y, lse = attend(q, batch, 4, 0)
+    batch.check(y, lse)

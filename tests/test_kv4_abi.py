@@ -146,3 +146,10 @@ def test_binding_refusals():
                 dict(n_pages=0), dict(n_kv=0)):
         with pytest.raises(ValueError):
             q.kv4_cache(**{**dict(n_pages=3, n_kv=2, head_dim=64, device="cpu"), **bad})
+
+
+def test_scales_whose_power_of_two_form_overflows(lib):
+    """The kernel multiplies by scale log2 e: infinite in float32 from 2.36e38 on, where every score would be no number."""
+    for scale in (2.4e38, 3e38, 3.4e38):
+        assert attend(lib, scale=scale) == EINVAL
+    assert attend(lib, scale=2.3e38, ws=None) == EWORKSPACE and attend(lib, scale=1e-45, ws=None) == EWORKSPACE
