@@ -40,21 +40,24 @@ KV4_SYMBOLS = tuple(_KV4_SIGS)
 
 _PLAIN = {torch.float32: LN_F32, torch.bfloat16: LN_BF16}
 _GROUPS, _DIMS = (32, 64, 128), (64, 128, 256)
+_MAX_PAGE, _MAX_HEADS = 4096, 1024
 _MOST = 2 ** 31 - 1  # ctypes takes larger ones modulo 2^32
 
 
 def kv4_cache(n_pages: int, n_kv: int, head_dim: int, page_size: int = 32, group: int = 64, device="cuda"):
     """(k_codes, k_scales, v_codes, v_scales) of an empty cache (all zeros) of n_pages pages of
-    page_size tokens (a multiple of 32), n_kv heads of head_dim (64, 128 or 256) values and a
+    page_size tokens (a multiple of 32 up to 4096), n_kv heads of head_dim (64, 128 or 256) values and a
     step and a least value to `group` of them (32, 64 or 128)."""
     if head_dim not in _DIMS:
         raise ValueError(f"head_dim must be 64, 128 or 256, got {head_dim}")
     if group not in _GROUPS or head_dim % group:
         raise ValueError(f"group must be 32, 64 or 128 and divide head_dim {head_dim}, got {group}")
-    if page_size < 32 or page_size % 32:
-        raise ValueError(f"page_size must be a multiple of 32, got {page_size}")
-    if n_pages < 1 or n_kv < 1:
-        raise ValueError("n_pages and n_kv must be at least 1")
+    if page_size < 32 or page_size % 32 or page_size > _MAX_PAGE:
+        raise ValueError(f"page_size must be a multiple of 32 up to {_MAX_PAGE}, got {page_size}")
+    if n_pages < 1 or not 1 <= n_kv <= _MAX_HEADS:
+        raise ValueError(f"n_pages must be at least 1 and n_kv 1 to {_MAX_HEADS}, got {n_pages} and {n_kv}")
+    if n_pages > _MOST or n_pages * page_size >= 1 << 40:
+        raise ValueError(f"n_pages must be below 2^31 and n_pages page_size below 2^40, got {n_pages} and {page_size}")
 
     def tensors(*codes):
         return (torch.zeros(n_pages, n_kv, *codes, dtype=torch.uint8, device=device),

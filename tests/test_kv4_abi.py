@@ -153,3 +153,13 @@ def test_scales_whose_power_of_two_form_overflows(lib):
     for scale in (2.4e38, 3e38, 3.4e38):
         assert attend(lib, scale=scale) == EINVAL
     assert attend(lib, scale=2.3e38, ws=None) == EWORKSPACE and attend(lib, scale=1e-45, ws=None) == EWORKSPACE
+
+
+def test_a_cache_that_no_call_takes_is_not_made():
+    """The entry points' limits, when the cache is made and not at its first use."""
+    import qlora_linear_amd as q
+    make = lambda **kw: q.kv4_cache(**{**dict(n_pages=1, n_kv=1, head_dim=64, device="meta"), **kw})  # noqa: E731
+    for bad in (dict(page_size=4128), dict(page_size=8192), dict(n_kv=1025), dict(n_pages=1 << 31), dict(n_pages=1 << 30, page_size=1024)):
+        with pytest.raises(ValueError):
+            make(**bad)
+    assert make(page_size=4096)[0].shape == (1, 1, 4096, 32) and make(n_kv=1024)[0].shape[1] == 1024
