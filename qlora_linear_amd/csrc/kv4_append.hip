@@ -195,8 +195,9 @@ __device__ __forceinline__ uint32_t coded8(const ln_kv4_cache& c, const uint4& b
 // fetches its own). The others take values: a thread N tokens of a head, whose codes are whole
 // words where the tokens fill four places that lie together. N is 1 for fewer than 512 tokens, so
 // that there are as many workgroups as can be, or 4.
-// 8192 tokens of 32 and 8 heads of 128 (184 MB) take 53 us, the vector units busy 65 % of it. With
-// the chunks of a tile's heads as the grid's fastest index it took 57.
+// 8192 tokens of 32 and 8 heads of 128 (187 MB) take 53 us, the vector units issuing in 71 % of the CUs'
+// cycles; 2047 tokens of 40 and 40 heads, groups of 32 (99 MB), 37 us, 81 %. With the chunks of a tile's heads
+// as the grid's fastest index the first took 57.
 template <int D, typename In, int N>
 __global__ __launch_bounds__(kThreads) void kv4_append_kernel(Kv4Append a, ln_kv4_cache c, int turned) {
   constexpr int kPieces = D / 8, kTile = tokens_of(D, N), kHeads = heads_of(D, N);

@@ -13,7 +13,7 @@
 // a lane's results are eight keys of one query. That is the operand of the second product as it
 // is, whose rows are elements of the head: nothing moves between lanes in a tile, and codes
 // reach the lanes that multiply them straight from global memory. m is raised only when a score
-// passes it by 2^8 (a vote); p then stays below 2^8, which costs no accuracy, and the cross-lane
+// passes it by 8 (a vote); p then stays below 2^8, which costs no accuracy, and the cross-lane
 // maximum and the rescaling drop out of most tiles.
 //
 // Row blocks, up to 16 NQ rows of one sequence and key head, are laid end to end in units of the
@@ -24,8 +24,10 @@
 //
 // What bounds it: with few rows the loads of this pattern and the vector units, by turns (64
 // sequences of up to 16384 keys, 554 MB: 114 us; when the kernel took 150, its loads alone took 113
-// and its arithmetic alone 110). Many rows are bound by the vector units, which overlap little with the
-// matrix units at two waves a SIMD (512 tokens against up to 16384 keys: 250 us, 549 TFLOP/s).
+// and its arithmetic alone 110; the vector units issue in 55 % of the CUs' cycles, the matrix units work
+// in 15 %). Many rows are bound by the vector units, which overlap little with the matrix units at two
+// waves a SIMD (512 tokens against up to 16384 keys: 252 us, 546 TFLOP/s, 70 % and 29 %; prompts of 2500
+// tokens 78 % and 26 %).
 // Measured and not kept, each against the build of its time: codes as 16 + c by shifts and masks, in
 // place of the conversion (64 sequences 128 -> 159 us); row blocks of 16 rows only (the chunk of
 // 512 tokens 1496 us, 261 with larger ones); twice the workers (1 x 131071 keys 46 -> 59 us).
@@ -63,8 +65,9 @@ __device__ __forceinline__ int64_t uniform(int64_t v) {
   return (static_cast<int64_t>(__builtin_amdgcn_readfirstlane(static_cast<int>(v >> 32))) << 32) | lo;
 }
 
-// Memory that no kernel of the call writes: a read at a shared place is a scalar one, and is not
-// counted with the loads of codes.
+// Memory that the kernel reading it does not write: a read at a shared place is a scalar one, and is not
+// counted with the loads of codes. (The lists of row blocks are written by the launch before; the scalar
+// cache is only sure to see that from the next launch on.)
 typedef const __attribute__((address_space(4))) int32_t* Const;
 
 struct Plan {
@@ -79,8 +82,8 @@ struct Plan {
   int cuts;
 };
 
-// Units of time: of a step, of one where 16 rows do (measured 5 : 2 of 64 rows, 3 : 2 of 32), of
-// a row block itself. tiles: a step's.
+// Units of time: of a step, of one where 16 rows do (measured 5 : 2 of 64 rows, 3 : 2 of 32; one set
+// for all head widths and groups), of a row block itself. tiles: a step's.
 struct Cost {
   int tiles, step, step16, block;
 };
