@@ -174,3 +174,127 @@ def test_far_keys_and_values(q, far):
     batch = u.Batch(3, [(1, 700), (4, 300)], 8, 2, 128, 64, 32, step=(0.2 * far, 0.4 * far), scale=0.1 / far)
     y, lse = attend(q, batch, 4, 0)
     batch.check(y, lse)
+
+
+# ---- sizes at their ends -------------------------------------------------------------------
+@pytest.mark.parametrize("seqs,n_q,n_kv,D,G,page", [
+    ([(1, 9000), (3, 4097), (1, 1)], 4, 2, 64, 32, 4096), ([(1, 2500), (40, 1057)], 2, 2, 128, 64, 1056),
+    ([(1, 70), (2, 33)], 1024, 1, 64, 64, 32), ([(1, 40), (1, 9)], 1024, 1024, 64, 32, 32), ([(3, 50)], 1024, 4, 256, 128, 32)])
+@pytest.mark.parametrize("bounded", [True, False])
+def test_largest_pages_and_heads(q, seqs, n_q, n_kv, D, G, page, bounded):
+    batch = u.Batch(len(seqs) + n_q, seqs, n_q, n_kv, D, G, page)
+    print("ends", seqs, n_q, n_kv, D, G, page, bounded, flush=True)
+    y, lse = attend(q, batch, max(n for n, _ in seqs) if bounded else 0, 0)
+    batch.check(y, lse)
+
+
+def test_very_many_sequences(q):
+    """Tokens of 100003 sequences, far more than a workgroup's threads, of one page each."""
+    B, D = 100003, 64
+    batch = u.Batch(1, [(1, 32)] * 40, 2, 1, D, 64, 32)
+    _, cache, table, _ = batch.device()
+    g = torch.Generator(device="cuda").manual_seed(2)
+    which = torch.randint(0, 40, (B,), generator=g, device="cuda")
+    lens = torch.randint(0, 33, (B,), generator=g, device="cuda", dtype=torch.int32)
+    x = torch.randn(B, 2, D, generator=g, device="cuda").bfloat16()
+    y, lse = q.kv4_attention(x, cache, table[which][:, :1].contiguous(), lens, return_lse=True)
+    assert bool((y[lens == 0] == 0).all()) and bool((lse[lens == 0] == -float("inf")).all())
+    at = [0, 1, 1023, 1024, 5000, 65535, 65536, B - 2, B - 1] + torch.randint(0, B, (300,), generator=g, device="cuda").tolist()
+    # The same tokens by themselves: p s is rounded about another m, half a step of bf16 of s |c - 8| <= 3.2 each, and
+    # y; a score is off by (2 64 + 8) U scale |q| |k|, |q| |k| at most 3 6 64 = 1152 with scale 1 / 8, each
+    for i in at:
+        one, l1 = q.kv4_attention(x[i:i + 1].clone(), cache, table[which[i:i + 1]][:, :1].contiguous(), lens[i:i + 1].clone(), return_lse=True)
+        assert torch.allclose(one.float(), y[i:i + 1].float(), rtol=2 * u.UB, atol=2 * u.UB * 3.2) and \
+            (int(lens[i]) == 0 or torch.allclose(l1, lse[i:i + 1], rtol=1e-6, atol=3e-3)), i
+
+
+@pytest.mark.parametrize("bounded", [True, False])
+def test_lists_of_no_rows(q, bounded):
+    """Row lists that name no row leave every row as it was."""
+    batch = u.Batch(5, [(3, 100), (2, 64)], 4, 2, 64, 32, 32)
+    x, cache, table, lens = batch.device()
+    for rows in ([0, 0, 0], [5, 5, 5], [2, 2, 2]):
+        out = torch.full((5, 4, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+        cu = torch.tensor(rows, dtype=torch.int32, device="cuda")
+        q.kv4_attention(x, cache, table, lens, cu_q=cu, max_q=3 if bounded else None, out=out)
+        assert bool((out == 7).all()), rows
+
+
+def test_more_rows_than_the_bound(q):
+    """Rows past max_q may be left as they were; those before it are right, and nothing else is written."""
+    batch = u.Batch(6, [(40, 300), (9, 64), (1, 20)], 6, 2, 128, 64, 32)
+    x, cache, table, lens = batch.device()
+    cu = torch.from_numpy(batch.cu).cuda()
+    wide = torch.full((50 + 8, 6, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    q.kv4_attention(x, cache, table, lens, cu_q=cu, max_q=9, out=wide[4:54])
+    assert bool((wide[:4] == 7).all()) and bool((wide[54:] == 7).all())
+    want = q.kv4_attention(x, cache, table, lens, cu_q=cu, max_q=40)
+    batch.check(want)
+    got = wide[4:54].clone()
+    got[9:40] = want[9:40]
+    batch.check(got)
+
+
+@pytest.mark.parametrize("T", [8192, 8193, 8200])
+def test_append_at_the_end_of_a_launch(q, T):
+    """A slot that a token of the last launch, of one token or of eight, has in common with earlier ones."""
+    D, n_kv = 128, 2
+    g = torch.Generator(device="cuda").manual_seed(T)
+    k, v = (torch.randn(T, n_kv, D, generator=g, device="cuda").bfloat16() for _ in range(2))
+    slots = torch.arange(T, device="cuda")
+    slots[T - 1], slots[8191], slots[8190] = 5, 5, 8191
+    a, b = (q.kv4_cache(T // 32 + 1, n_kv, D, 32, 32) for _ in range(2))
+    q.kv4_append(None, k, v, a, slots)
+    last = {s: t for t, s in enumerate(slots.tolist())}
+    keep = torch.tensor(sorted(last.values()), device="cuda")
+    for part in keep.split(300):
+        q.kv4_append(None, k[part], v[part], b, slots[part])
+    assert all(torch.equal(s, t) for s, t in zip(a, b))
+
+
+@pytest.mark.parametrize("bound", [None, 12])
+def test_captured_ragged(q, bound):
+    """Ragged rows captured once and replayed as the rows' places and the lengths change in their tensors, with eager
+    calls between, in a workspace that a decode of other sizes also uses."""
+    plans = [[(12, 500), (0, 0), (3, 90), (1, 700)], [(1, 1), (12, 12), (2, 640), (1, 33)], [(0, 5), (0, 0), (0, 9), (16 - 4, 300)],
+             [(5, 650), (5, 651), (5, 652), (1, 300)]]
+    batches = [u.Batch(60 + i, s, 8, 2, 64, 32, 64, width=11) for i, s in enumerate(plans)]
+    made = [b.device() for b in batches]
+    T, pages = 16, max(m[1][0].shape[0] for m in made)
+    cache = q.kv4_cache(pages, 2, 64, 64, 32)
+    x, table = torch.zeros(T, 8, 64, dtype=torch.bfloat16, device="cuda"), torch.zeros(4, 11, dtype=torch.int32, device="cuda")
+    lens, cu = torch.zeros(4, dtype=torch.int32, device="cuda"), torch.zeros(5, dtype=torch.int32, device="cuda")
+    need = q.kv4_attention_workspace_bytes(T, 4, 8, 2, 64, bound or 0, 11, 64)
+    ws = torch.empty(max(need, q.kv4_attention_workspace_bytes(1, 1, 8, 2, 64, 1, 11, 64)), dtype=torch.uint8, device="cuda")
+
+    def place(i):
+        m, b = made[i], batches[i]
+        x.zero_()
+        x[:b.q.shape[0]] = m[0]
+        for to, part in zip(cache, m[1]):
+            to[:part.shape[0]] = part
+        table.copy_(m[2].masked_fill(m[2] >= m[1][0].shape[0], -1))
+        lens.copy_(m[3])
+        cu.copy_(torch.from_numpy(b.cu))
+
+    out = torch.zeros_like(x)
+    run = lambda y, w: q.kv4_attention(x, cache, table, lens, cu_q=cu, max_q=bound, out=y, workspace=w)  # noqa: E731
+    place(0)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        run(out, ws)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run(out, ws)
+    for n in range(9):
+        i = (2 * n + n // 4) % 4
+        place(i)
+        rows = int(batches[i].cu[-1])
+        want = run(torch.zeros_like(x), None)
+        q.kv4_attention(x[:1].contiguous(), cache, table[:1].contiguous(), lens[:1].contiguous(), workspace=ws)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out[:rows], want[:rows]), (n, i)
+        batches[i].check(out[:rows])
